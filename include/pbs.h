@@ -80,7 +80,11 @@ typedef struct CUstream_st* pbs_stream_t;
 #define PBS_DEVERR_TABLE     16  /* a prebuilt table row the kernel cannot read: ctx outside
                                     [0, topk_k * 128], or (prefill tile kernel) a slot whose page ids
                                     are not page_table[r][b] * block_page_stride + j of a block b of
-                                    the row's request (the row attends nothing) */
+                                    the row's request (the row attends nothing). Block operations: a
+                                    row index outside the table, a row too short for its tokens, a
+                                    block released more often than it is held, a row naming a free
+                                    block (see each entry) */
+#define PBS_DEVERR_NO_BLOCK  32  /* reserve / fork: no free block left (see the entry) */
 
 /* ---- KV cache formats -------------------------------------------------------------------- */
 #define PBS_KV_BF16      0  /* page = [Hkv][16 rows][K(head_dim) | V(head_dim)] bf16 ([flashinfer]: K|V
@@ -415,6 +419,171 @@ PBS_API int pbs_insert_index_cache(
     const void* index_k, int64_t k_stride0, int64_t k_stride1, int32_t num_tokens, int32_t dim,
     void* index_cache, int64_t c_stride0, int64_t c_stride1, int32_t num_blocks, int32_t block_tokens,
     const int64_t* slot_mapping, int64_t slot_stride, int32_t elem_bytes,
+    int32_t* err_word, pbs_stream_t stream);
+
+/*
+ * Window attend with sinks, decode rows: attention over the paged cache without a top-k list, for
+ * layers that read a sliding window plus the first tokens of the request, or (window = 0) all of
+ * it, beside the block-sparse layers on the same cache. No counterpart on the pages.
+ *
+ * Row r sits at abs_pos as in pbs_sparse_decode_attention and sees key n of its request iff
+ *   0 <= n <= abs_pos  and  (window == 0  or  n > abs_pos - window  or  n < num_sinks).
+ * Arguments, layouts, formats, GQA ratios, scales and lse as there, except:
+ *   page_table   [batch, max_blocks] physical block ids: key n lies at page
+ *                page_table[r / decode_query_len][n / 128] * block_page_stride + n % 128 / 16, row
+ *                n % 16. Entries of blocks no row sees are not read (they may be -1: released).
+ *   window       keys the window spans, the row's own among them; 0: no limit; < 0: PBS_ERR_ARG.
+ *   num_sinks    first keys that stay visible (>= 0).
+ * A row that sees no key (abs_pos < 0) gets zeros and lse -inf: padded rows may have seq_len 0. A
+ * visible key whose block is past the page table (PBS_DEVERR_BLOCK_OOB) or whose page is negative or
+ * past the cache (PBS_DEVERR_PAGE_OOB) is left out; the row's other keys are attended. What masked
+ * keys hold (infinities, NaN) does not reach a row that does not see them.
+ *   workspace    optional (NULL, 0): pbs_window_decode_workspace_bytes() bytes or more, 16-byte
+ *                aligned, zeroed once before first use; with it the keys of all rows are dealt evenly to
+ *                the GPU's CTAs and a request cut between CTAs is merged through it (its tickets are
+ *                zero again when the call completes; too small: PBS_ERR_SHAPE). Without it one CTA takes all
+ *                keys of its rows. Calls that share one workspace must not run concurrently.
+ */
+PBS_API int pbs_window_decode_attention(
+    const void* q, int64_t q_row_stride, int64_t q_head_stride,
+    const void* kv_cache, int64_t page_stride_bytes, int64_t num_pages, int32_t kv_dtype,
+    int32_t num_heads, int32_t num_kv_heads, int32_t head_dim,
+    const int32_t* page_table, int64_t pt_row_stride, int32_t max_blocks,
+    const int32_t* seq_lens, int32_t batch, int32_t decode_query_len, int32_t block_page_stride,
+    int32_t window, int32_t num_sinks,
+    float softmax_scale, float k_scale, float v_scale,
+    void* out, int64_t out_row_stride, int64_t out_head_stride,
+    float* lse, int64_t lse_row_stride,
+    void* workspace, size_t workspace_bytes,
+    int32_t* err_word, pbs_stream_t stream);
+
+/* Bytes of pbs_window_decode_attention's workspace on the current device (0: bad arguments). */
+PBS_API size_t pbs_window_decode_workspace_bytes(int32_t batch, int32_t decode_query_len, int32_t num_heads,
+                                                 int32_t num_kv_heads);
+
+/*
+ * Window attend with sinks, varlen prefill: token positions as in pbs_sparse_prefill_attention, the
+ * visible keys, page table, errors and lse as in pbs_window_decode_attention. Rows at or behind
+ * cu_seqlens_q[num_reqs] are left as they were (a batch padded to total_q rows).
+ *   workspace    optional (NULL, 0): pbs_window_prefill_workspace_bytes() bytes or more, 256-byte
+ *                aligned, no initial value; with it (and 16-byte aligned q / out rows, GQA ratios as
+ *                above) the call runs on the tcgen05 kernel, otherwise on the decode kernel (mma.sync). A
+ *                smaller one is not used. Calls that share one workspace must not run concurrently.
+ * On the tcgen05 kernel a key is multiplied for every token of its query tile (128 / G tokens of one
+ * request): a non-finite V row reaches the tile's tokens that do not see it when a neighbour does.
+ */
+PBS_API int pbs_window_prefill_attention(
+    const void* q, int64_t q_row_stride, int64_t q_head_stride,
+    const void* kv_cache, int64_t page_stride_bytes, int64_t num_pages, int32_t kv_dtype,
+    int32_t num_heads, int32_t num_kv_heads, int32_t head_dim,
+    const int32_t* page_table, int64_t pt_row_stride, int32_t max_blocks,
+    const int32_t* cu_seqlens_q, const int32_t* seq_lens, int32_t num_reqs, int32_t total_q,
+    int32_t block_page_stride, int32_t window, int32_t num_sinks,
+    float softmax_scale, float k_scale, float v_scale,
+    void* out, int64_t out_row_stride, int64_t out_head_stride,
+    float* lse, int64_t lse_row_stride,
+    void* workspace, size_t workspace_bytes,
+    int32_t* err_word, pbs_stream_t stream);
+
+/* Bytes of pbs_window_prefill_attention's workspace (0: bad arguments). */
+PBS_API size_t pbs_window_prefill_workspace_bytes(int32_t total_q, int32_t num_reqs, int32_t num_kv_heads,
+                                                  int32_t max_blocks, int32_t kv_dtype, int32_t window,
+                                                  int32_t num_sinks);
+
+/*
+ * K/V insert: the K and V rows of new tokens into the cache, in its format. For n < num_tokens and
+ * slot = slot_mapping[n * slot_stride], the rows of every kv head go to page
+ * (slot / 128) * block_page_stride + slot % 128 / 16, row slot % 16 (slot = page_table[r][p / 128] *
+ * 128 + p % 128 for position p of request r). A negative slot is padding and is skipped; a slot
+ * whose page is >= num_pages sets PBS_DEVERR_SLOT_OOB and is skipped. Slots must be distinct. The
+ * counterpart of pbs_insert_index_cache for the cache the attends read.
+ *
+ *   k, v         [num_tokens, num_kv_heads, 128] bf16, strides in elements (any; 16-byte aligned
+ *                rows with unit dim stride are fastest)
+ *   k_scale, v_scale  finite, not 0: bf16 stores the elements as they are and ignores them; fp8 stores
+ *                e4m3(x / scale), saturating; NVFP4 stores per 16 elements s = e4m3(max|x / scale| / 6) and
+ *                e2m1(x / scale / s), both to nearest even, saturating (s = 0: zeros; a NaN makes its
+ *                16 values NaN). The attends multiply by the same scales.
+ */
+PBS_API int pbs_insert_kv_cache(
+    const void* k, int64_t k_row_stride, int64_t k_head_stride, int64_t k_dim_stride,
+    const void* v, int64_t v_row_stride, int64_t v_head_stride, int64_t v_dim_stride,
+    int32_t num_tokens, int32_t num_kv_heads, int32_t head_dim,
+    void* kv_cache, int64_t page_stride_bytes, int64_t num_pages, int32_t kv_dtype, int32_t block_page_stride,
+    const int64_t* slot_mapping, int64_t slot_stride, float k_scale, float v_scale,
+    int32_t* err_word, pbs_stream_t stream);
+
+/*
+ * Block operations. A pool of num_blocks physical blocks: block b is pages b * block_page_stride ..
+ * + block_page_stride - 1 of every layer (layer l's page p at kv_cache + l * layer_stride_bytes + p *
+ * page_stride_bytes, page_bytes of it in use; all multiples of 16 bytes, else PBS_ERR_ALIGN).
+ * page_table [num_rows, max_blocks] holds block ids (-1: none), ref_counts [num_blocks] how many
+ * table entries (or other holders of the caller's) name each block, 0: free. Allocation takes the
+ * lowest free ids, in the order of the call's rows: results do not depend on the order in which the
+ * GPU runs. One call at a time may change a pool; bytes move in unspecified order, so within one call
+ * no block (row) may be both read and written, or written twice.
+ */
+
+/* Block src_blocks[i] of every layer to dst_blocks[i], i < n. A negative id skips the pair; an id >=
+ * num_pages / block_page_stride sets PBS_DEVERR_BLOCK_OOB and skips it. */
+PBS_API int pbs_copy_cache_blocks(
+    void* kv_cache, int64_t layer_stride_bytes, int32_t num_layers, int64_t page_stride_bytes, int64_t page_bytes,
+    int64_t num_pages, int32_t block_page_stride, const int32_t* src_blocks, const int32_t* dst_blocks, int32_t n,
+    int32_t* err_word, pbs_stream_t stream);
+
+/*
+ * Room for new tokens: for each i in order, every missing (negative) entry of row rows[i] that covers
+ * positions seq_lens .. seq_lens + new_tokens[i] - 1 gets a free block (count 1), then seq_lens[rows[i]]
+ * += new_tokens[i]. Rows must be distinct. No free block left: PBS_DEVERR_NO_BLOCK, the row's length
+ * stays and its remaining entries stay missing (the blocks it got stay). A row index outside the table,
+ * a negative count or more tokens than the row has entries for: PBS_DEVERR_TABLE, row skipped.
+ */
+PBS_API int pbs_reserve_cache_blocks(
+    int32_t* page_table, int64_t pt_row_stride, int32_t num_rows, int32_t max_blocks, int32_t* seq_lens,
+    int32_t* ref_counts, int32_t num_blocks, const int32_t* rows, const int32_t* new_tokens, int32_t n,
+    int32_t* err_word, pbs_stream_t stream);
+
+/*
+ * Fork: row dst_rows[i] becomes a copy of row src_rows[i]: same length, its full blocks shared (counts
+ * + 1; missing entries stay missing), a partly filled last block copied (every layer) into a free
+ * block, so that both may append. What dst_rows held before is overwritten, not released. dst_rows
+ * must be distinct and none of them a source. copy_src, copy_dst [n]: the copied pairs (negative: none).
+ * No free block left: PBS_DEVERR_NO_BLOCK, that child becomes an empty row of length 0. A row index
+ * outside the table, or a row forked onto itself: PBS_DEVERR_TABLE, pair skipped. num_blocks must be
+ * at most num_pages / block_page_stride.
+ */
+PBS_API int pbs_fork_cache(
+    void* kv_cache, int64_t layer_stride_bytes, int32_t num_layers, int64_t page_stride_bytes, int64_t page_bytes,
+    int64_t num_pages, int32_t block_page_stride,
+    int32_t* page_table, int64_t pt_row_stride, int32_t num_rows, int32_t max_blocks, int32_t* seq_lens,
+    int32_t* ref_counts, int32_t num_blocks, const int32_t* src_rows, const int32_t* dst_rows, int32_t n,
+    int32_t* copy_src, int32_t* copy_dst, int32_t* err_word, pbs_stream_t stream);
+
+/*
+ * Release: gives back blocks of rows rows[i] (counts - 1, entries become -1). window = 0: all of them,
+ * and the row's length becomes 0. window > 0: those that no query at position seq_lens[row] or later
+ * sees under pbs_window_decode_attention's rule for this window and num_sinks; the length stays. A row
+ * listed twice gives its blocks back once. A row index outside the table or a block whose count is
+ * already 0: PBS_DEVERR_TABLE; an id >= num_blocks: PBS_DEVERR_BLOCK_OOB (the entry is cleared).
+ */
+PBS_API int pbs_release_cache_blocks(
+    int32_t* page_table, int64_t pt_row_stride, int32_t num_rows, int32_t max_blocks, int32_t* seq_lens,
+    int32_t* ref_counts, int32_t num_blocks, const int32_t* rows, int32_t n, int32_t window, int32_t num_sinks,
+    int32_t* err_word, pbs_stream_t stream);
+
+/*
+ * Compact: moves the live blocks (count > 0) to ids 0 .. live - 1. The i-th live block at an id >= live
+ * moves (every layer) to the i-th free id below live; the others stay. Rewrites page_table and
+ * ref_counts, and writes remap [num_blocks] (each block's new id, -1 for a free one: for holders
+ * outside page_table) and counts [2] (live blocks, blocks moved). scratch: 2 * num_blocks int32.
+ * A row that names a free block: PBS_DEVERR_TABLE, the entry becomes -1; an id >= num_blocks:
+ * PBS_DEVERR_BLOCK_OOB, the entry stays. num_blocks as in pbs_fork_cache.
+ */
+PBS_API int pbs_compact_cache(
+    void* kv_cache, int64_t layer_stride_bytes, int32_t num_layers, int64_t page_stride_bytes, int64_t page_bytes,
+    int64_t num_pages, int32_t block_page_stride,
+    int32_t* page_table, int64_t pt_row_stride, int32_t num_rows, int32_t max_blocks, int32_t* ref_counts,
+    int32_t num_blocks, int32_t* remap, int32_t* counts, int32_t* scratch,
     int32_t* err_word, pbs_stream_t stream);
 
 #ifdef __cplusplus

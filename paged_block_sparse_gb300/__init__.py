@@ -23,13 +23,16 @@ __all__ = [
     "attend_workspace_bytes", "attend_workspace", "sparse_decode_attention_noalloc", "sparse_mixed_attention",
     "prefill_workspace_bytes", "prefill_workspace", "prefill_tile_workspace_bytes", "prefill_tile_workspace",
     "prefill_kernel_choice", "PREFILL_KERNELS",
+    "window_decode_attention", "window_prefill_attention", "window_decode_workspace_bytes",
+    "window_prefill_workspace_bytes", "insert_kv_cache", "copy_cache_blocks", "reserve_cache_blocks", "fork_cache",
+    "release_cache_blocks", "compact_cache",
 ]
 
 SPARSE_BLOCK_SIZE = 128
 PAGE_ROWS = 16
 PAGES_PER_BLOCK = 8
 KV_DTYPES = {"bf16": 0, "fp8_e4m3": 1, "nvfp4": 2}
-DEVERR = {"block_oob": 1, "page_oob": 2, "slot_oob": 4, "timeout": 8, "table": 16}
+DEVERR = {"block_oob": 1, "page_oob": 2, "slot_oob": 4, "timeout": 8, "table": 16, "no_block": 32}
 # prefill kernels (pbs_attend_options.prefill_kernel / pbs_prefill_kernel_choice)
 PREFILL_KERNELS = {"auto": 0, "token": 1, "tile": 2, "gather": 3}
 _PREFILL_NAMES = {v: k for k, v in PREFILL_KERNELS.items()}
@@ -100,7 +103,31 @@ def lib() -> ctypes.CDLL:
         f32, f32, f32, vp, i64, i64, vp, i64, vp, ctypes.c_size_t, vp, vp, vp]
     L.pbs_insert_index_cache.restype = ctypes.c_int
     L.pbs_insert_index_cache.argtypes = [vp, i64, i64, i32, i32, vp, i64, i64, i32, i32, vp, i64, i32, vp, vp]
-    del sz
+    window_head = [vp, i64, i64, vp, i64, i64, i32, i32, i32, i32, vp, i64, i32]
+    window_tail = [i32, i32, i32, f32, f32, f32, vp, i64, i64, vp, i64, vp, sz, vp, vp]
+    L.pbs_window_decode_attention.restype = ctypes.c_int
+    L.pbs_window_decode_attention.argtypes = window_head + [vp, i32, i32] + window_tail
+    L.pbs_window_prefill_attention.restype = ctypes.c_int
+    L.pbs_window_prefill_attention.argtypes = window_head + [vp, vp, i32, i32] + window_tail
+    L.pbs_window_decode_workspace_bytes.restype = sz
+    L.pbs_window_decode_workspace_bytes.argtypes = [i32] * 4
+    L.pbs_window_prefill_workspace_bytes.restype = sz
+    L.pbs_window_prefill_workspace_bytes.argtypes = [i32] * 7
+    L.pbs_insert_kv_cache.restype = ctypes.c_int
+    L.pbs_insert_kv_cache.argtypes = [vp, i64, i64, i64] * 2 + [i32, i32, i32, vp, i64, i64, i32, i32, vp, i64, f32,
+                                                               f32, vp, vp]
+    pool = [vp, i64, i32, i64, i64, i64, i32]
+    rows = [vp, i64, i32, i32]
+    L.pbs_copy_cache_blocks.restype = ctypes.c_int
+    L.pbs_copy_cache_blocks.argtypes = pool + [vp, vp, i32, vp, vp]
+    L.pbs_reserve_cache_blocks.restype = ctypes.c_int
+    L.pbs_reserve_cache_blocks.argtypes = rows + [vp, vp, i32, vp, vp, i32, vp, vp]
+    L.pbs_fork_cache.restype = ctypes.c_int
+    L.pbs_fork_cache.argtypes = pool + rows + [vp, vp, i32, vp, vp, i32, vp, vp, vp, vp]
+    L.pbs_release_cache_blocks.restype = ctypes.c_int
+    L.pbs_release_cache_blocks.argtypes = rows + [vp, vp, i32, vp, i32, i32, i32, vp, vp]
+    L.pbs_compact_cache.restype = ctypes.c_int
+    L.pbs_compact_cache.argtypes = pool + rows + [vp, i32, vp, vp, vp, vp, vp]
     _lib = L
     return L
 
@@ -571,3 +598,288 @@ def insert_index_cache(index_k, index_cache, index_slot_mapping, err_word=None, 
         _ptr(index_slot_mapping), index_slot_mapping.stride(0), index_k.element_size(), _ptr(err_word),
         _stream(stream, index_k.device))
     _check(st, "pbs_insert_index_cache")
+
+
+# --------------------------------------------------------------------------------------------
+# window attends, K/V insert and block operations on the same cache
+# --------------------------------------------------------------------------------------------
+
+def _call(device, fn, where, *args):
+    """fn(*args) with `device` current (the library launches on the current device)."""
+    if torch.cuda.current_device() == device.index:
+        st = fn(*args)
+    else:
+        with torch.cuda.device(device):
+            st = fn(*args)
+    if st != 0:
+        raise PbsError(st, where)
+
+
+def _vec(t, name, device, dtype=torch.int32):
+    """data_ptr of a contiguous vector of `dtype` on `device`."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if t.dim() != 1 or (t.shape[0] > 1 and t.stride(0) != 1):
+        raise ValueError(f"{name} must be a contiguous vector")
+    return t.data_ptr()
+
+
+def _err(err_word, device):
+    return None if err_word is None else _vec(err_word, "err_word", device)
+
+
+def _raw_stream(stream, device):
+    return (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+
+
+def _empty(shape, dtype, device, stream):
+    """A new tensor that belongs to the stream the call runs on."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def _table(t, name, device):
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    return _table2d(t, name)
+
+
+_window_workspaces: dict = {}
+
+
+def window_decode_workspace_bytes(batch: int, decode_query_len: int, num_heads: int, num_kv_heads: int) -> int:
+    """Bytes of :func:`window_decode_attention`'s workspace (zeroed once before first use)."""
+    return int(lib().pbs_window_decode_workspace_bytes(int(batch), int(decode_query_len), int(num_heads),
+                                                       int(num_kv_heads)))
+
+
+def window_prefill_workspace_bytes(total_q: int, num_reqs: int, num_kv_heads: int, max_blocks: int,
+                                   kv_dtype: str = "bf16", window: int = 0, num_sinks: int = 0) -> int:
+    """Bytes of :func:`window_prefill_attention`'s workspace (no initial value)."""
+    return int(lib().pbs_window_prefill_workspace_bytes(int(total_q), int(num_reqs), int(num_kv_heads),
+                                                        int(max_blocks), KV_DTYPES[kv_dtype], int(window),
+                                                        int(num_sinks)))
+
+
+def _window_workspace(kind, need, device, stream):
+    """The cached workspace of (kind, device, stream), grown on demand. Calls on one stream run in
+    order, so they may share it; a call under graph capture gets memory of the graph's own, so that
+    graphs captured on one stream may be replayed side by side."""
+    s = torch.cuda.current_stream(device) if stream is None else stream
+    make = torch.zeros if kind == "decode" else torch.empty
+    with torch.cuda.stream(s):
+        if torch.cuda.is_current_stream_capturing():
+            return make(need, dtype=torch.uint8, device=device)
+        key = (kind, device.index, s.cuda_stream)
+        ws = _window_workspaces.get(key)
+        if ws is None or ws.numel() < need:
+            _window_workspaces.pop(key, None)
+            ws = make(max(need, 1 << 20), dtype=torch.uint8, device=device)
+            _window_workspaces[key] = ws
+    return ws
+
+
+def _window_prologue(q, kv_cache, kv_dtype, page_table, seq_lens, out, lse, return_lse, stream):
+    _dev(q, "q", torch.bfloat16, 3)
+    dev = q.device
+    if q.dim() != 3 or (q.shape[2] > 1 and q.stride(2) != 1):
+        raise ValueError("q must be [rows, Hq, 128] with a contiguous head_dim")
+    if kv_dtype not in KV_DTYPES:
+        raise ValueError(f"kv_dtype must be one of {sorted(KV_DTYPES)}")
+    if kv_cache.device != dev:
+        raise ValueError(f"kv_cache must be on {dev}, got {kv_cache.device}")
+    pt = _table(page_table, "page_table", dev)
+    if pt.shape[0] != seq_lens.shape[0]:
+        raise ValueError(f"page_table has {pt.shape[0]} rows for {seq_lens.shape[0]} requests")
+    if out is None:
+        out = _empty(q.shape, torch.bfloat16, dev, stream)
+    elif out.dtype != torch.bfloat16 or out.device != dev or out.shape != q.shape or out.stride(2) != 1:
+        raise ValueError("out must be bf16 of q's shape on q's device with a contiguous head_dim")
+    if lse is None and return_lse:
+        lse = _empty(q.shape[:2], torch.float32, dev, stream)
+    elif lse is not None and lse.device != dev:
+        raise ValueError(f"lse must be on {dev}, got {lse.device}")
+    return dev, pt, out, _lse_arg(lse, False, q)
+
+
+def window_decode_attention(q, kv_cache, kv_dtype: str, num_kv_heads: int, page_table, seq_lens,
+                            decode_query_len: int, softmax_scale: float, window: int = 0, num_sinks: int = 0,
+                            k_scale: float = 1.0, v_scale: float = 1.0, block_page_stride: int = PAGES_PER_BLOCK,
+                            out=None, err_word=None, stream=None, workspace="auto", lse=None,
+                            return_lse: bool = False):
+    """Attention of decode rows over the paged cache without a top-k list: a query at position p sees
+    the keys n <= p of its request with n > p - window (any n when ``window`` is 0) or n < num_sinks.
+
+    q [rows, Hq, 128] bf16, rows = len(seq_lens) * decode_query_len, right-aligned to seq_lens;
+    page_table [batch, max_blocks] int32 (entries of blocks that no row sees may be -1). Returns out (and
+    lse, as in :func:`sparse_decode_attention`). ``workspace``: "auto" (cached per stream, or the
+    graph's own memory under capture), None (each request's keys on one CTA per kv head) or a zeroed uint8
+    tensor of :func:`window_decode_workspace_bytes` bytes."""
+    dev, pt, out, lse = _window_prologue(q, kv_cache, kv_dtype, page_table, seq_lens, out, lse, return_lse, stream)
+    L = lib()
+    batch, dql, hq, hkv = seq_lens.shape[0], int(decode_query_len), q.shape[1], int(num_kv_heads)
+    if q.shape[0] != batch * dql:
+        raise ValueError(f"q has {q.shape[0]} rows for {batch} requests of {dql}")
+    if isinstance(workspace, str):
+        if workspace != "auto":
+            raise ValueError('workspace must be "auto", None or a uint8 CUDA tensor')
+        need = int(L.pbs_window_decode_workspace_bytes(batch, dql, hq, hkv))
+        workspace = _window_workspace("decode", need, dev, stream) if need else None
+    wp, wb = (None, 0) if workspace is None else (_vec(workspace, "workspace", dev, torch.uint8), workspace.numel())
+    _call(dev, L.pbs_window_decode_attention, "pbs_window_decode_attention",
+          q.data_ptr(), q.stride(0), q.stride(1), kv_cache.data_ptr(), kv_cache.stride(0) * kv_cache.element_size(),
+          kv_cache.shape[0], KV_DTYPES[kv_dtype], hq, hkv, q.shape[2], pt.data_ptr(), pt.stride(0), pt.shape[1],
+          _vec(seq_lens, "seq_lens", dev), batch, dql, int(block_page_stride), int(window), int(num_sinks),
+          softmax_scale, k_scale, v_scale, out.data_ptr(), out.stride(0), out.stride(1),
+          None if lse is None else lse.data_ptr(), 0 if lse is None else lse.stride(0), wp, wb, _err(err_word, dev),
+          _raw_stream(stream, dev))
+    return out if lse is None else (out, lse)
+
+
+def window_prefill_attention(q, kv_cache, kv_dtype: str, num_kv_heads: int, page_table, cu_seqlens_q, seq_lens,
+                             softmax_scale: float, window: int = 0, num_sinks: int = 0, k_scale: float = 1.0,
+                             v_scale: float = 1.0, block_page_stride: int = PAGES_PER_BLOCK, out=None, err_word=None,
+                             stream=None, workspace="auto", lse=None, return_lse: bool = False):
+    """:func:`window_decode_attention`'s rule for the tokens of varlen prefill requests (positions as
+    in :func:`sparse_prefill_attention`). Rows of q behind cu_seqlens_q[-1] are left as they were in
+    ``out``. ``workspace``: "auto", None (the mma.sync kernel) or a uint8 tensor of
+    :func:`window_prefill_workspace_bytes` bytes."""
+    dev, pt, out, lse = _window_prologue(q, kv_cache, kv_dtype, page_table, seq_lens, out, lse, return_lse, stream)
+    L = lib()
+    reqs, hkv = seq_lens.shape[0], int(num_kv_heads)
+    if cu_seqlens_q.shape[0] != reqs + 1:
+        raise ValueError(f"cu_seqlens_q must hold {reqs + 1} entries for {reqs} requests")
+    if isinstance(workspace, str):
+        if workspace != "auto":
+            raise ValueError('workspace must be "auto", None or a uint8 CUDA tensor')
+        need = int(L.pbs_window_prefill_workspace_bytes(q.shape[0], reqs, hkv, pt.shape[1], KV_DTYPES[kv_dtype],
+                                                        int(window), int(num_sinks)))
+        workspace = _window_workspace("prefill", need, dev, stream) if need else None
+    wp, wb = (None, 0) if workspace is None else (_vec(workspace, "workspace", dev, torch.uint8), workspace.numel())
+    _call(dev, L.pbs_window_prefill_attention, "pbs_window_prefill_attention",
+          q.data_ptr(), q.stride(0), q.stride(1), kv_cache.data_ptr(), kv_cache.stride(0) * kv_cache.element_size(),
+          kv_cache.shape[0], KV_DTYPES[kv_dtype], q.shape[1], hkv, q.shape[2], pt.data_ptr(), pt.stride(0),
+          pt.shape[1], _vec(cu_seqlens_q, "cu_seqlens_q", dev), _vec(seq_lens, "seq_lens", dev), reqs, q.shape[0],
+          int(block_page_stride), int(window), int(num_sinks), softmax_scale, k_scale, v_scale, out.data_ptr(),
+          out.stride(0), out.stride(1), None if lse is None else lse.data_ptr(),
+          0 if lse is None else lse.stride(0), wp, wb, _err(err_word, dev), _raw_stream(stream, dev))
+    return out if lse is None else (out, lse)
+
+
+def insert_kv_cache(k, v, kv_cache, kv_dtype: str, slot_mapping, k_scale: float = 1.0, v_scale: float = 1.0,
+                    block_page_stride: int = PAGES_PER_BLOCK, err_word=None, stream=None) -> None:
+    """Write the K and V rows [N, Hkv, 128] bf16 (any strides) of new tokens into the cache in its
+    format; slot_mapping [N] int64 = physical block * 128 + offset, negative: skipped."""
+    _dev(k, "k", torch.bfloat16, 3)
+    dev = k.device
+    if v.dtype != torch.bfloat16 or v.device != dev or v.shape != k.shape or k.dim() != 3:
+        raise ValueError("k and v must be bf16 [N, Hkv, 128] on one device")
+    if kv_dtype not in KV_DTYPES:
+        raise ValueError(f"kv_dtype must be one of {sorted(KV_DTYPES)}")
+    if kv_cache.device != dev or slot_mapping.device != dev:
+        raise ValueError(f"kv_cache and slot_mapping must be on {dev}")
+    if slot_mapping.dtype != torch.int64 or slot_mapping.dim() != 1 or slot_mapping.shape[0] != k.shape[0]:
+        raise ValueError("slot_mapping must be a length-N int64 vector")
+    _call(dev, lib().pbs_insert_kv_cache, "pbs_insert_kv_cache",
+          k.data_ptr(), k.stride(0), k.stride(1), k.stride(2), v.data_ptr(), v.stride(0), v.stride(1), v.stride(2),
+          k.shape[0], k.shape[1], k.shape[2], kv_cache.data_ptr(), kv_cache.stride(0) * kv_cache.element_size(),
+          kv_cache.shape[0], KV_DTYPES[kv_dtype], int(block_page_stride), slot_mapping.data_ptr(),
+          slot_mapping.stride(0), k_scale, v_scale, _err(err_word, dev), _raw_stream(stream, dev))
+
+
+def _pool(kv_cache):
+    """(device, pool arguments) of a cache [num_pages, page elements] or [layers, num_pages, page elements]."""
+    _dev(kv_cache, "kv_cache")
+    if kv_cache.dim() not in (2, 3) or (kv_cache.shape[-1] > 1 and kv_cache.stride(-1) != 1):
+        raise ValueError("kv_cache must be [pages, page] or [layers, pages, page] with contiguous pages")
+    eb = kv_cache.element_size()
+    layers, layer_stride = (1, 0) if kv_cache.dim() == 2 else (kv_cache.shape[0], kv_cache.stride(0) * eb)
+    return kv_cache.device, (kv_cache.data_ptr(), layer_stride, layers, kv_cache.stride(-2) * eb,
+                             kv_cache.shape[-1] * eb, kv_cache.shape[-2])
+
+
+def _rows_args(page_table, device):
+    pt = _table(page_table, "page_table", device)
+    return pt.data_ptr(), pt.stride(0), pt.shape[0], pt.shape[1]
+
+
+def _lens_of(seq_lens, page_table, device):
+    p = _vec(seq_lens, "seq_lens", device)
+    if seq_lens.shape[0] != page_table.shape[0]:
+        raise ValueError(f"seq_lens must hold page_table's {page_table.shape[0]} rows")
+    return p
+
+
+def copy_cache_blocks(kv_cache, src_blocks, dst_blocks, block_page_stride: int = PAGES_PER_BLOCK, err_word=None,
+                      stream=None) -> None:
+    """Copy block src_blocks[i] of every layer to dst_blocks[i] (int32; a negative id skips the pair).
+    kv_cache [pages, page] or [layers, pages, page]. No block may be both a source and a destination."""
+    dev, pool = _pool(kv_cache)
+    s, d = _vec(src_blocks, "src_blocks", dev), _vec(dst_blocks, "dst_blocks", dev)
+    if src_blocks.shape != dst_blocks.shape:
+        raise ValueError("src_blocks and dst_blocks must be of one length")
+    _call(dev, lib().pbs_copy_cache_blocks, "pbs_copy_cache_blocks", *pool, int(block_page_stride), s, d,
+          src_blocks.shape[0], _err(err_word, dev), _raw_stream(stream, dev))
+
+
+def reserve_cache_blocks(page_table, seq_lens, ref_counts, rows, new_tokens, err_word=None, stream=None) -> None:
+    """Give each row rows[i] (int32, distinct) blocks for new_tokens[i] more tokens, the lowest free ids
+    first, and add them to its length (see ``pbs_reserve_cache_blocks`` for a pool that runs out)."""
+    dev = page_table.device
+    table = _rows_args(page_table, dev)
+    r, t = _vec(rows, "rows", dev), _vec(new_tokens, "new_tokens", dev)
+    if rows.shape != new_tokens.shape:
+        raise ValueError("rows and new_tokens must be of one length")
+    _call(dev, lib().pbs_reserve_cache_blocks, "pbs_reserve_cache_blocks", *table,
+          _lens_of(seq_lens, page_table, dev), _vec(ref_counts, "ref_counts", dev), ref_counts.shape[0], r, t,
+          rows.shape[0], _err(err_word, dev), _raw_stream(stream, dev))
+
+
+def fork_cache(kv_cache, page_table, seq_lens, ref_counts, src_rows, dst_rows,
+               block_page_stride: int = PAGES_PER_BLOCK, err_word=None, stream=None):
+    """Make row dst_rows[i] a copy of row src_rows[i]: full blocks shared (counts + 1), a partly filled
+    last block copied into a free one, in every layer. Returns the copied pairs (src, dst), negative
+    where a child has none."""
+    dev, pool = _pool(kv_cache)
+    table = _rows_args(page_table, dev)
+    s, d = _vec(src_rows, "src_rows", dev), _vec(dst_rows, "dst_rows", dev)
+    if src_rows.shape != dst_rows.shape:
+        raise ValueError("src_rows and dst_rows must be of one length")
+    n = src_rows.shape[0]
+    pairs = _empty((2, n), torch.int32, dev, stream)
+    _call(dev, lib().pbs_fork_cache, "pbs_fork_cache", *pool, int(block_page_stride), *table,
+          _lens_of(seq_lens, page_table, dev), _vec(ref_counts, "ref_counts", dev), ref_counts.shape[0], s, d, n,
+          pairs.data_ptr(), pairs.data_ptr() + 4 * n, _err(err_word, dev), _raw_stream(stream, dev))
+    return pairs[0], pairs[1]
+
+
+def release_cache_blocks(page_table, seq_lens, ref_counts, rows, window: int = 0, num_sinks: int = 0, err_word=None,
+                         stream=None) -> None:
+    """Give back the blocks of rows (int32): all of them (``window`` 0; the length becomes 0), or those that
+    no query at position seq_lens[row] or later sees through the window and its sinks."""
+    dev = page_table.device
+    _call(dev, lib().pbs_release_cache_blocks, "pbs_release_cache_blocks", *_rows_args(page_table, dev),
+          _lens_of(seq_lens, page_table, dev), _vec(ref_counts, "ref_counts", dev), ref_counts.shape[0],
+          _vec(rows, "rows", dev), rows.shape[0], int(window), int(num_sinks), _err(err_word, dev),
+          _raw_stream(stream, dev))
+
+
+def compact_cache(kv_cache, page_table, ref_counts, block_page_stride: int = PAGES_PER_BLOCK, err_word=None,
+                  stream=None):
+    """Move the pool's live blocks to the ids 0 .. live - 1 in every layer and rewrite page_table and
+    ref_counts. Returns (remap [num_blocks] int32: each block's new id, -1 for a free one; the number of
+    live blocks, an int32 scalar on the device)."""
+    dev, pool = _pool(kv_cache)
+    nb = ref_counts.shape[0]
+    buf = _empty((3 * nb + 2,), torch.int32, dev, stream)
+    p = buf.data_ptr()
+    _call(dev, lib().pbs_compact_cache, "pbs_compact_cache", *pool, int(block_page_stride),
+          *_rows_args(page_table, dev), _vec(ref_counts, "ref_counts", dev), nb, p, p + 4 * nb, p + 4 * (nb + 2),
+          _err(err_word, dev), _raw_stream(stream, dev))
+    return buf[:nb], buf[nb]

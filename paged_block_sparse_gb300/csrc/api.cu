@@ -936,4 +936,304 @@ int pbs_insert_index_cache(const void* index_k, int64_t k_stride0, int64_t k_str
                                                                                                   : PBS_ERR_CUDA;
 }
 
+// ---- window attends --------------------------------------------------------------------------
+
+static int make_window_args(pbs::WindowArgs* w, const void* q, int64_t q_row_stride, int64_t q_head_stride,
+                            const void* kv_cache, int64_t page_stride_bytes, int64_t num_pages, int32_t kv_dtype,
+                            int32_t num_heads, int32_t num_kv_heads, int32_t head_dim, const int32_t* page_table,
+                            int64_t pt_row_stride, int32_t max_blocks, const int32_t* seq_lens,
+                            int32_t block_page_stride, int32_t window, int32_t num_sinks, float softmax_scale,
+                            float k_scale, float v_scale, void* out, int64_t out_row_stride, int64_t out_head_stride,
+                            float* lse, int64_t lse_row_stride, void* workspace, size_t workspace_bytes,
+                            int32_t* err_word) {
+  int st = check_attend(q, q_row_stride, q_head_stride, kv_cache, page_stride_bytes, num_pages, kv_dtype, num_heads,
+                        num_kv_heads, head_dim, softmax_scale, k_scale, v_scale, out, out_row_stride, out_head_stride);
+  if (st != PBS_OK) return st;
+  if (page_table == nullptr || seq_lens == nullptr || max_blocks <= 0) return PBS_ERR_ARG;
+  if (pt_row_stride < max_blocks || block_page_stride < kBlockPages) return PBS_ERR_SHAPE;
+  if (window < 0 || num_sinks < 0) return PBS_ERR_ARG;
+  if (workspace == nullptr && workspace_bytes != 0) return PBS_ERR_ARG;
+  if (lse != nullptr) {
+    if (!aligned(lse, 4)) return PBS_ERR_ALIGN;
+    if (lse_row_stride < num_heads) return PBS_ERR_SHAPE;
+  }
+  *w = pbs::WindowArgs();
+  w->q = static_cast<const uint16_t*>(q);
+  w->q_row_stride = q_row_stride;
+  w->q_head_stride = q_head_stride;
+  w->kv_cache = static_cast<const uint8_t*>(kv_cache);
+  w->page_stride_bytes = page_stride_bytes;
+  w->num_pages = num_pages;
+  w->kv_dtype = kv_dtype;
+  w->num_heads = num_heads;
+  w->num_kv_heads = num_kv_heads;
+  w->group = num_heads / num_kv_heads;
+  w->page_table = page_table;
+  w->pt_row_stride = pt_row_stride;
+  w->max_blocks = max_blocks;
+  w->seq_lens = seq_lens;
+  w->block_page_stride = block_page_stride;
+  w->window = window;
+  w->num_sinks = num_sinks;
+  w->scale_log2 = static_cast<float>(static_cast<double>(softmax_scale) * k_scale * 1.4426950408889634);
+  w->v_scale = v_scale;
+  w->out = static_cast<uint16_t*>(out);
+  w->out_row_stride = out_row_stride;
+  w->out_head_stride = out_head_stride;
+  w->lse = lse;
+  w->lse_row_stride = lse_row_stride;
+  w->err_word = err_word;
+  return PBS_OK;
+}
+
+int pbs_window_decode_attention(const void* q, int64_t q_row_stride, int64_t q_head_stride, const void* kv_cache,
+                                int64_t page_stride_bytes, int64_t num_pages, int32_t kv_dtype, int32_t num_heads,
+                                int32_t num_kv_heads, int32_t head_dim, const int32_t* page_table,
+                                int64_t pt_row_stride, int32_t max_blocks, const int32_t* seq_lens, int32_t batch,
+                                int32_t decode_query_len, int32_t block_page_stride, int32_t window, int32_t num_sinks,
+                                float softmax_scale, float k_scale, float v_scale, void* out, int64_t out_row_stride,
+                                int64_t out_head_stride, float* lse, int64_t lse_row_stride, void* workspace,
+                                size_t workspace_bytes, int32_t* err_word, pbs_stream_t stream) {
+  if (batch < 0 || decode_query_len <= 0) return PBS_ERR_ARG;
+  const int64_t rows = static_cast<int64_t>(batch) * decode_query_len;
+  if (rows == 0) return PBS_OK;
+  if (rows > 0x7fffffffLL / 16) return PBS_ERR_UNSUPPORTED;
+  pbs::WindowArgs w;
+  int st = make_window_args(&w, q, q_row_stride, q_head_stride, kv_cache, page_stride_bytes, num_pages, kv_dtype,
+                            num_heads, num_kv_heads, head_dim, page_table, pt_row_stride, max_blocks, seq_lens,
+                            block_page_stride, window, num_sinks, softmax_scale, k_scale, v_scale, out, out_row_stride,
+                            out_head_stride, lse, lse_row_stride, workspace, workspace_bytes, err_word);
+  if (st != PBS_OK) return st;
+  if (workspace != nullptr && !aligned(workspace, 16)) return PBS_ERR_ALIGN;
+  if (workspace != nullptr &&
+      workspace_bytes < pbs_window_decode_workspace_bytes(batch, decode_query_len, num_heads, num_kv_heads))
+    return PBS_ERR_SHAPE;
+  w.num_reqs = batch;
+  w.decode_query_len = decode_query_len;
+  w.num_rows = static_cast<int32_t>(rows);
+  return pbs::launch_window_attend(w, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? PBS_OK : PBS_ERR_CUDA;
+}
+
+size_t pbs_window_decode_workspace_bytes(int32_t batch, int32_t decode_query_len, int32_t num_heads,
+                                         int32_t num_kv_heads) {
+  if (batch <= 0 || decode_query_len <= 0 || num_heads <= 0 || num_kv_heads <= 0 || num_heads % num_kv_heads != 0)
+    return 0;
+  return 16;
+}
+
+int pbs_window_prefill_attention(const void* q, int64_t q_row_stride, int64_t q_head_stride, const void* kv_cache,
+                                 int64_t page_stride_bytes, int64_t num_pages, int32_t kv_dtype, int32_t num_heads,
+                                 int32_t num_kv_heads, int32_t head_dim, const int32_t* page_table,
+                                 int64_t pt_row_stride, int32_t max_blocks, const int32_t* cu_seqlens_q,
+                                 const int32_t* seq_lens, int32_t num_reqs, int32_t total_q, int32_t block_page_stride,
+                                 int32_t window, int32_t num_sinks, float softmax_scale, float k_scale, float v_scale,
+                                 void* out, int64_t out_row_stride, int64_t out_head_stride, float* lse,
+                                 int64_t lse_row_stride, void* workspace, size_t workspace_bytes, int32_t* err_word,
+                                 pbs_stream_t stream) {
+  if (total_q < 0 || num_reqs < 0) return PBS_ERR_ARG;
+  if (total_q == 0) return PBS_OK;
+  if (num_reqs == 0) return PBS_ERR_SHAPE;
+  if (cu_seqlens_q == nullptr) return PBS_ERR_ARG;
+  if (total_q > 0x7fffffff / 16) return PBS_ERR_UNSUPPORTED;
+  pbs::WindowArgs w;
+  int st = make_window_args(&w, q, q_row_stride, q_head_stride, kv_cache, page_stride_bytes, num_pages, kv_dtype,
+                            num_heads, num_kv_heads, head_dim, page_table, pt_row_stride, max_blocks, seq_lens,
+                            block_page_stride, window, num_sinks, softmax_scale, k_scale, v_scale, out, out_row_stride,
+                            out_head_stride, lse, lse_row_stride, workspace, workspace_bytes, err_word);
+  if (st != PBS_OK) return st;
+  w.cu_seqlens_q = cu_seqlens_q;
+  w.num_reqs = num_reqs;
+  w.decode_query_len = 1;
+  w.num_rows = total_q;
+  return pbs::launch_window_attend(w, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? PBS_OK : PBS_ERR_CUDA;
+}
+
+size_t pbs_window_prefill_workspace_bytes(int32_t total_q, int32_t num_reqs, int32_t num_kv_heads, int32_t max_blocks,
+                                          int32_t kv_dtype, int32_t window, int32_t num_sinks) {
+  if (total_q <= 0 || num_reqs <= 0 || num_kv_heads <= 0 || max_blocks <= 0 || window < 0 || num_sinks < 0 ||
+      kv_dtype < PBS_KV_BF16 || kv_dtype > PBS_KV_NVFP4)
+    return 0;
+  return 256;
+}
+
+// ---- K/V insert and block operations ---------------------------------------------------------
+
+int pbs_insert_kv_cache(const void* k, int64_t k_row_stride, int64_t k_head_stride, int64_t k_dim_stride,
+                        const void* v, int64_t v_row_stride, int64_t v_head_stride, int64_t v_dim_stride,
+                        int32_t num_tokens, int32_t num_kv_heads, int32_t head_dim, void* kv_cache,
+                        int64_t page_stride_bytes, int64_t num_pages, int32_t kv_dtype, int32_t block_page_stride,
+                        const int64_t* slot_mapping, int64_t slot_stride, float k_scale, float v_scale,
+                        int32_t* err_word, pbs_stream_t stream) {
+  if (num_tokens < 0) return PBS_ERR_ARG;
+  if (num_tokens == 0) return PBS_OK;
+  if (k == nullptr || v == nullptr || kv_cache == nullptr || slot_mapping == nullptr) return PBS_ERR_ARG;
+  if (kv_dtype != PBS_KV_BF16 && kv_dtype != PBS_KV_FP8_E4M3 && kv_dtype != PBS_KV_NVFP4) return PBS_ERR_ARG;
+  if (num_kv_heads <= 0 || head_dim <= 0) return PBS_ERR_ARG;
+  if (!std::isfinite(k_scale) || !std::isfinite(v_scale) || k_scale == 0.f || v_scale == 0.f) return PBS_ERR_ARG;
+  if (head_dim != kHeadDim || num_kv_heads > 65535) return PBS_ERR_UNSUPPORTED;
+  if (k_row_stride < 0 || k_head_stride < 0 || k_dim_stride < 0 || v_row_stride < 0 || v_head_stride < 0 ||
+      v_dim_stride < 0 || slot_stride < 0 || block_page_stride < kBlockPages)
+    return PBS_ERR_SHAPE;
+  if (num_pages <= 0 || page_stride_bytes < page_content_bytes(kv_dtype, num_kv_heads)) return PBS_ERR_SHAPE;
+  if (!aligned(kv_cache, 16) || page_stride_bytes % 16 != 0 || !aligned(k, 2) || !aligned(v, 2) ||
+      !aligned(slot_mapping, 8))
+    return PBS_ERR_ALIGN;
+  pbs::KvInsertArgs a = {};
+  a.k = static_cast<const uint16_t*>(k);
+  a.k_row_stride = k_row_stride;
+  a.k_head_stride = k_head_stride;
+  a.k_dim_stride = k_dim_stride;
+  a.v = static_cast<const uint16_t*>(v);
+  a.v_row_stride = v_row_stride;
+  a.v_head_stride = v_head_stride;
+  a.v_dim_stride = v_dim_stride;
+  a.num_tokens = num_tokens;
+  a.num_kv_heads = num_kv_heads;
+  a.kv_cache = static_cast<uint8_t*>(kv_cache);
+  a.page_stride_bytes = page_stride_bytes;
+  a.num_pages = num_pages;
+  a.kv_dtype = kv_dtype;
+  a.block_page_stride = block_page_stride;
+  a.slot_mapping = slot_mapping;
+  a.slot_stride = slot_stride;
+  a.inv_k_scale = static_cast<float>(1.0 / k_scale);
+  a.inv_v_scale = static_cast<float>(1.0 / v_scale);
+  a.err_word = err_word;
+  return pbs::launch_kv_insert(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? PBS_OK : PBS_ERR_CUDA;
+}
+
+// The pool's geometry, checked; num_blocks <= 0 takes every block of the cache.
+static int attach_pool(pbs::BlockArgs* a, void* kv_cache, int64_t layer_stride_bytes, int32_t num_layers,
+                       int64_t page_stride_bytes, int64_t page_bytes, int64_t num_pages, int32_t block_page_stride,
+                       int32_t num_blocks) {
+  if (kv_cache == nullptr || num_layers <= 0 || num_pages <= 0 || page_bytes <= 0) return PBS_ERR_ARG;
+  if (block_page_stride < kBlockPages || page_stride_bytes < page_bytes) return PBS_ERR_SHAPE;
+  if (num_layers > 1 && layer_stride_bytes < page_bytes) return PBS_ERR_SHAPE;
+  const int64_t fit = num_pages / block_page_stride;
+  if (fit > 0x7fffffffLL || num_blocks > fit) return PBS_ERR_SHAPE;
+  if (!aligned(kv_cache, 16) || layer_stride_bytes % 16 != 0 || page_stride_bytes % 16 != 0 || page_bytes % 16 != 0)
+    return PBS_ERR_ALIGN;
+  a->kv_cache = static_cast<uint8_t*>(kv_cache);
+  a->layer_stride_bytes = layer_stride_bytes;
+  a->num_layers = num_layers;
+  a->page_stride_bytes = page_stride_bytes;
+  a->block_page_stride = block_page_stride;
+  a->num_blocks = num_blocks > 0 ? num_blocks : static_cast<int32_t>(fit);
+  const bool packed = page_bytes == page_stride_bytes;
+  a->pages_per_unit = packed ? block_page_stride : 1;
+  a->unit_bytes = packed ? page_bytes * block_page_stride : page_bytes;
+  return PBS_OK;
+}
+
+static int attach_rows(pbs::BlockArgs* a, int32_t* page_table, int64_t pt_row_stride, int32_t num_rows,
+                       int32_t max_blocks, int32_t* seq_lens, bool lens_needed, int32_t* ref_counts,
+                       int32_t num_blocks) {
+  if (page_table == nullptr || ref_counts == nullptr || (lens_needed && seq_lens == nullptr)) return PBS_ERR_ARG;
+  if (num_rows <= 0 || max_blocks <= 0 || num_blocks <= 0) return PBS_ERR_ARG;
+  if (pt_row_stride < max_blocks) return PBS_ERR_SHAPE;
+  if (!aligned(page_table, 4) || !aligned(ref_counts, 4) || !aligned(seq_lens, 4)) return PBS_ERR_ALIGN;
+  a->page_table = page_table;
+  a->pt_row_stride = pt_row_stride;
+  a->num_rows = num_rows;
+  a->max_blocks = max_blocks;
+  a->seq_lens = seq_lens;
+  a->ref_counts = ref_counts;
+  a->num_blocks = num_blocks;
+  return PBS_OK;
+}
+
+int pbs_copy_cache_blocks(void* kv_cache, int64_t layer_stride_bytes, int32_t num_layers, int64_t page_stride_bytes,
+                          int64_t page_bytes, int64_t num_pages, int32_t block_page_stride, const int32_t* src_blocks,
+                          const int32_t* dst_blocks, int32_t n, int32_t* err_word, pbs_stream_t stream) {
+  if (n < 0) return PBS_ERR_ARG;
+  if (n == 0) return PBS_OK;
+  if (src_blocks == nullptr || dst_blocks == nullptr) return PBS_ERR_ARG;
+  pbs::BlockArgs a = {};
+  int st = attach_pool(&a, kv_cache, layer_stride_bytes, num_layers, page_stride_bytes, page_bytes, num_pages,
+                       block_page_stride, 0);
+  if (st != PBS_OK) return st;
+  a.src_rows = src_blocks;
+  a.dst_rows = dst_blocks;
+  a.n = n;
+  a.err_word = err_word;
+  return pbs::launch_copy_blocks(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? PBS_OK : PBS_ERR_CUDA;
+}
+
+int pbs_reserve_cache_blocks(int32_t* page_table, int64_t pt_row_stride, int32_t num_rows, int32_t max_blocks,
+                             int32_t* seq_lens, int32_t* ref_counts, int32_t num_blocks, const int32_t* rows,
+                             const int32_t* new_tokens, int32_t n, int32_t* err_word, pbs_stream_t stream) {
+  if (n < 0) return PBS_ERR_ARG;
+  if (n == 0) return PBS_OK;
+  if (rows == nullptr || new_tokens == nullptr) return PBS_ERR_ARG;
+  pbs::BlockArgs a = {};
+  int st = attach_rows(&a, page_table, pt_row_stride, num_rows, max_blocks, seq_lens, true, ref_counts, num_blocks);
+  if (st != PBS_OK) return st;
+  a.dst_rows = rows;
+  a.new_tokens = new_tokens;
+  a.n = n;
+  a.err_word = err_word;
+  return pbs::launch_reserve_blocks(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? PBS_OK : PBS_ERR_CUDA;
+}
+
+int pbs_fork_cache(void* kv_cache, int64_t layer_stride_bytes, int32_t num_layers, int64_t page_stride_bytes,
+                   int64_t page_bytes, int64_t num_pages, int32_t block_page_stride, int32_t* page_table,
+                   int64_t pt_row_stride, int32_t num_rows, int32_t max_blocks, int32_t* seq_lens, int32_t* ref_counts,
+                   int32_t num_blocks, const int32_t* src_rows, const int32_t* dst_rows, int32_t n, int32_t* copy_src,
+                   int32_t* copy_dst, int32_t* err_word, pbs_stream_t stream) {
+  if (n < 0) return PBS_ERR_ARG;
+  if (n == 0) return PBS_OK;
+  if (src_rows == nullptr || dst_rows == nullptr || copy_src == nullptr || copy_dst == nullptr) return PBS_ERR_ARG;
+  pbs::BlockArgs a = {};
+  int st = attach_rows(&a, page_table, pt_row_stride, num_rows, max_blocks, seq_lens, true, ref_counts, num_blocks);
+  if (st != PBS_OK) return st;
+  st = attach_pool(&a, kv_cache, layer_stride_bytes, num_layers, page_stride_bytes, page_bytes, num_pages,
+                   block_page_stride, num_blocks);
+  if (st != PBS_OK) return st;
+  a.src_rows = src_rows;
+  a.dst_rows = dst_rows;
+  a.n = n;
+  a.copy_src = copy_src;
+  a.copy_dst = copy_dst;
+  a.err_word = err_word;
+  return pbs::launch_fork(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? PBS_OK : PBS_ERR_CUDA;
+}
+
+int pbs_release_cache_blocks(int32_t* page_table, int64_t pt_row_stride, int32_t num_rows, int32_t max_blocks,
+                             int32_t* seq_lens, int32_t* ref_counts, int32_t num_blocks, const int32_t* rows, int32_t n,
+                             int32_t window, int32_t num_sinks, int32_t* err_word, pbs_stream_t stream) {
+  if (n < 0 || window < 0 || num_sinks < 0) return PBS_ERR_ARG;
+  if (n == 0) return PBS_OK;
+  if (rows == nullptr) return PBS_ERR_ARG;
+  pbs::BlockArgs a = {};
+  int st = attach_rows(&a, page_table, pt_row_stride, num_rows, max_blocks, seq_lens, true, ref_counts, num_blocks);
+  if (st != PBS_OK) return st;
+  if (static_cast<int64_t>(n) * max_blocks > (int64_t(1) << 38)) return PBS_ERR_UNSUPPORTED;
+  a.dst_rows = rows;
+  a.n = n;
+  a.window = window;
+  a.num_sinks = num_sinks;
+  a.err_word = err_word;
+  return pbs::launch_release(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? PBS_OK : PBS_ERR_CUDA;
+}
+
+int pbs_compact_cache(void* kv_cache, int64_t layer_stride_bytes, int32_t num_layers, int64_t page_stride_bytes,
+                      int64_t page_bytes, int64_t num_pages, int32_t block_page_stride, int32_t* page_table,
+                      int64_t pt_row_stride, int32_t num_rows, int32_t max_blocks, int32_t* ref_counts,
+                      int32_t num_blocks, int32_t* remap, int32_t* counts, int32_t* scratch, int32_t* err_word,
+                      pbs_stream_t stream) {
+  if (remap == nullptr || counts == nullptr || scratch == nullptr) return PBS_ERR_ARG;
+  pbs::BlockArgs a = {};
+  int st = attach_rows(&a, page_table, pt_row_stride, num_rows, max_blocks, nullptr, false, ref_counts, num_blocks);
+  if (st != PBS_OK) return st;
+  st = attach_pool(&a, kv_cache, layer_stride_bytes, num_layers, page_stride_bytes, page_bytes, num_pages,
+                   block_page_stride, num_blocks);
+  if (st != PBS_OK) return st;
+  a.remap = remap;
+  a.counts = counts;
+  a.copy_src = scratch;
+  a.copy_dst = scratch + num_blocks;
+  a.err_word = err_word;
+  return pbs::launch_compact(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? PBS_OK : PBS_ERR_CUDA;
+}
+
 }  // extern "C"

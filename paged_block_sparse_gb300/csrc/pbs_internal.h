@@ -200,4 +200,78 @@ struct InsertArgs {
 
 cudaError_t launch_insert_index_cache(const InsertArgs& a, cudaStream_t stream);
 
+// K/V insert (kv_insert.cu).
+struct KvInsertArgs {
+  const uint16_t* k;  // bf16 bits [num_tokens, num_kv_heads, 128], strides in elements
+  int64_t k_row_stride, k_head_stride, k_dim_stride;
+  const uint16_t* v;
+  int64_t v_row_stride, v_head_stride, v_dim_stride;
+  int32_t num_tokens, num_kv_heads;
+  uint8_t* kv_cache;
+  int64_t page_stride_bytes, num_pages;
+  int32_t kv_dtype, block_page_stride;
+  const int64_t* slot_mapping;
+  int64_t slot_stride;
+  float inv_k_scale, inv_v_scale;
+  int32_t* err_word;
+};
+
+cudaError_t launch_kv_insert(const KvInsertArgs& a, cudaStream_t stream);
+
+// Block operations (cache_blocks.cu); each launcher reads the fields its entry point documents.
+struct BlockArgs {
+  uint8_t* kv_cache;
+  int64_t layer_stride_bytes, page_stride_bytes;
+  int32_t num_layers, block_page_stride, num_blocks;
+  int32_t pages_per_unit;  // contiguous pages copied as one run: 1, or all of a block's
+  int64_t unit_bytes;      // bytes of one run
+  int32_t* page_table;
+  int64_t pt_row_stride;
+  int32_t num_rows, max_blocks;
+  int32_t* seq_lens;
+  int32_t* ref_counts;
+  const int32_t* src_rows;  // fork's rows, or the copy's source blocks
+  const int32_t* dst_rows;  // fork / reserve / release rows, or the copy's destination blocks
+  const int32_t* new_tokens;
+  int32_t n;
+  int32_t window, num_sinks;
+  int32_t* copy_src;  // pairs a planning kernel leaves for the copy
+  int32_t* copy_dst;
+  int32_t* remap;
+  int32_t* counts;    // compact: [live blocks, moves]
+  int32_t* err_word;
+};
+
+cudaError_t launch_copy_blocks(const BlockArgs& a, cudaStream_t stream);
+cudaError_t launch_reserve_blocks(const BlockArgs& a, cudaStream_t stream);
+cudaError_t launch_fork(const BlockArgs& a, cudaStream_t stream);
+cudaError_t launch_release(const BlockArgs& a, cudaStream_t stream);
+cudaError_t launch_compact(const BlockArgs& a, cudaStream_t stream);
+
+// Window attend (window_attend.cu): decode rows (cu_seqlens_q null) or varlen prefill tokens.
+struct WindowArgs {
+  const uint16_t* q;
+  int64_t q_row_stride, q_head_stride;
+  const uint8_t* kv_cache;
+  int64_t page_stride_bytes, num_pages;
+  int32_t kv_dtype, num_heads, num_kv_heads, group;
+  const int32_t* page_table;
+  int64_t pt_row_stride;
+  int32_t max_blocks;
+  const int32_t* seq_lens;
+  const int32_t* cu_seqlens_q;
+  int32_t num_reqs, decode_query_len, num_rows;
+  int32_t block_page_stride;
+  int32_t window;     // 0: no limit
+  int32_t num_sinks;
+  float scale_log2, v_scale;
+  uint16_t* out;
+  int64_t out_row_stride, out_head_stride;
+  float* lse;
+  int64_t lse_row_stride;
+  int32_t* err_word;
+};
+
+cudaError_t launch_window_attend(const WindowArgs& a, cudaStream_t stream);
+
 }  // namespace pbs
