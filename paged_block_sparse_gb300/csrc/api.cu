@@ -986,6 +986,21 @@ static int make_window_args(pbs::WindowArgs* w, const void* q, int64_t q_row_str
   return PBS_OK;
 }
 
+// Pages a CTA of the split decode kernel takes at least: fewer than four per consumer warp cost
+// more in merging than the extra CTAs save.
+constexpr int32_t kWindowMinPages = 16;
+
+static int launch_window(const pbs::WindowArgs& w, int sms, pbs_stream_t stream) {
+  CUtensorMap map;
+  int32_t packed = 0;
+  const int st = encode_attend_map(&map, w.kv_cache, w.kv_dtype, w.num_kv_heads, w.num_pages, w.page_stride_bytes,
+                                   false, &packed);
+  if (st != PBS_OK) return st;
+  return pbs::launch_window_attend(w, map, packed != 0, sms, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+             ? PBS_OK
+             : PBS_ERR_CUDA;
+}
+
 int pbs_window_decode_attention(const void* q, int64_t q_row_stride, int64_t q_head_stride, const void* kv_cache,
                                 int64_t page_stride_bytes, int64_t num_pages, int32_t kv_dtype, int32_t num_heads,
                                 int32_t num_kv_heads, int32_t head_dim, const int32_t* page_table,
@@ -1005,20 +1020,31 @@ int pbs_window_decode_attention(const void* q, int64_t q_row_stride, int64_t q_h
                             out_head_stride, lse, lse_row_stride, workspace, workspace_bytes, err_word);
   if (st != PBS_OK) return st;
   if (workspace != nullptr && !aligned(workspace, 16)) return PBS_ERR_ALIGN;
-  if (workspace != nullptr &&
-      workspace_bytes < pbs_window_decode_workspace_bytes(batch, decode_query_len, num_heads, num_kv_heads))
-    return PBS_ERR_SHAPE;
   w.num_reqs = batch;
   w.decode_query_len = decode_query_len;
   w.num_rows = static_cast<int32_t>(rows);
-  return pbs::launch_window_attend(w, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? PBS_OK : PBS_ERR_CUDA;
+  pbs::window_geometry(&w, decode_query_len);
+  const int sms = num_sms();
+  if (workspace != nullptr) {
+    const int64_t units = static_cast<int64_t>(batch) * w.groups_per_req * num_kv_heads;
+    if (workspace_bytes < pbs::window_workspace_bytes(sms, units)) return PBS_ERR_SHAPE;
+    w.split_ws = static_cast<float*>(workspace);
+    w.split_tickets = static_cast<int32_t*>(workspace) + (workspace_bytes / sizeof(int32_t) - static_cast<size_t>(units));
+    w.min_pages = kWindowMinPages;
+  }
+  return launch_window(w, sms, stream);
 }
 
 size_t pbs_window_decode_workspace_bytes(int32_t batch, int32_t decode_query_len, int32_t num_heads,
                                          int32_t num_kv_heads) {
   if (batch <= 0 || decode_query_len <= 0 || num_heads <= 0 || num_kv_heads <= 0 || num_heads % num_kv_heads != 0)
     return 0;
-  return 16;
+  pbs::WindowArgs w = {};
+  w.group = num_heads / num_kv_heads;
+  w.decode_query_len = decode_query_len;
+  if (w.group > 16) return 0;
+  pbs::window_geometry(&w, decode_query_len);
+  return pbs::window_workspace_bytes(num_sms(), static_cast<int64_t>(batch) * w.groups_per_req * num_kv_heads);
 }
 
 int pbs_window_prefill_attention(const void* q, int64_t q_row_stride, int64_t q_head_stride, const void* kv_cache,
@@ -1043,9 +1069,10 @@ int pbs_window_prefill_attention(const void* q, int64_t q_row_stride, int64_t q_
   if (st != PBS_OK) return st;
   w.cu_seqlens_q = cu_seqlens_q;
   w.num_reqs = num_reqs;
-  w.decode_query_len = 1;
   w.num_rows = total_q;
-  return pbs::launch_window_attend(w, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? PBS_OK : PBS_ERR_CUDA;
+  w.decode_query_len = 1;
+  pbs::window_geometry(&w, 16);
+  return launch_window(w, num_sms(), stream);
 }
 
 size_t pbs_window_prefill_workspace_bytes(int32_t total_q, int32_t num_reqs, int32_t num_kv_heads, int32_t max_blocks,

@@ -270,8 +270,19 @@ struct WindowArgs {
   float* lse;
   int64_t lse_row_stride;
   int32_t* err_word;
+  int32_t rows_per_group;   // consecutive rows of a request that share the K / V reads
+  int32_t groups_per_req;   // decode
+  float* split_ws;          // non-null: the page sequence is cut evenly between the CTAs
+  int32_t* split_tickets;   // one per (group, kv head), zero between calls
+  int32_t min_pages;        // pages a CTA takes at least
 };
 
-cudaError_t launch_window_attend(const WindowArgs& a, cudaStream_t stream);
+// Sets rows_per_group and groups_per_req for requests of up to max_rows rows.
+void window_geometry(WindowArgs* a, int max_rows);
+// Workspace of the split: partials from the front, tickets in the last bytes.
+size_t window_workspace_bytes(int sms, int64_t units);
+// `tmap`: as for launch_attend (packed: the 5-D one-box-per-(page, head) map).
+cudaError_t launch_window_attend(const WindowArgs& a, const CUtensorMap& tmap, bool packed, int sms,
+                                 cudaStream_t stream);
 
 }  // namespace pbs

@@ -1,116 +1,648 @@
-// Window attend with sinks over the paged cache: every key n <= p of the query's request with
-// n > p - window (or any n when window is 0) or n < num_sinks.
+// Window attend with sinks over the paged cache, mma.sync kernel: decode rows, and prefill tokens
+// where the tcgen05 kernel does not run. For a query at position p of its request,
+//   out = v_scale * softmax(softmax_scale * k_scale * q K^T) V  over the keys
+//   0 <= n <= p with n > p - window (any n when window is 0) or n < num_sinks.
 //
-// One CTA per (row, query head), four warps striding over the visible keys, one key at a time:
-// lane l holds dims 4l .. 4l + 3. fp32 throughout, online softmax per warp, one merge.
+// Units. A group is up to 8 NT / G consecutive rows of one request (G query heads per kv head): its
+// rows x heads are the 8 NT columns of the MMAs, so the rows of a request share every K / V read. An
+// item is a group; its page list is [0, head pages) and then the window's pages up to the last
+// row's own, padded to an even count. A unit is (item, kv head).
+//
+// Work split. Bound by HBM (bf16, fp8) or by the dequantisation's issue slots (NVFP4), and lengths are
+// ragged, so with a workspace the pages of all units form one sequence that is cut into equal parts, one
+// per resident CTA: every CTA streams the same number of pages, whatever the batch. A CTA's part may end
+// one unit, hold whole ones and begin another; a unit cut between CTAs leaves one partial (max, sum, O)
+// per CTA in the workspace, and the CTA that draws the unit's last ticket merges them in page order
+// (the same bits whoever is last) and clears the ticket. Without a workspace a CTA takes one unit.
+//
+// CTA. One producer warp: page-table entries 32 pages at a time, one TMA box (bf16 / fp8) or bulk copy
+// (NVFP4) per page into a ring of kStages; it runs ahead across unit borders. kWarps consumer warps take
+// pairs of pages in turn (a stage always belongs to one warp), each with its own online softmax
+// (base 2, lazy reference: O is rescaled when the maximum passes it by 2^8); their partials meet in shared
+// memory at the end of a unit. S^T = K Q^T and O^T += V^T P^T with keys as MMA rows (window_page.cuh).
 #include "pbs_device.cuh"
 #include "pbs_internal.h"
+#include "window_page.cuh"
 
 namespace pbs {
 namespace {
 
-constexpr int kWarps = 4;
+constexpr int kWarps = 4;              // consumer warps
+constexpr int kThreads = 32 * (kWarps + 1);
+constexpr int kPair = 2;               // pages per consumer iteration
+constexpr float kLazyLog2 = 8.0f;
+constexpr int kOPitch = kHeadDim + 4;  // floats: rows 4 banks apart (conflict-free partial writes)
 
-__device__ __forceinline__ float half_of(uint32_t h2, int hi) {
-  float f;
-  const uint16_t h = static_cast<uint16_t>(hi ? h2 >> 16 : h2);
-  asm("cvt.f32.f16 %0, %1;" : "=f"(f) : "h"(h));
-  return f;
-}
+// bf16: 64 KiB of stages per CTA, 2 CTAs per SM; NVFP4: 36 KiB and 3 CTAs (its warps are busy with
+// dequantisation).
+template <int FMT>
+constexpr int kStages = FMT == PBS_KV_BF16 ? 8 : 16;
+template <int FMT>
+constexpr int kCtasPerSm = FMT == PBS_KV_NVFP4 ? 3 : 2;
+static_assert(kStages<PBS_KV_BF16> % (kPair * kWarps) == 0 && kStages<PBS_KV_NVFP4> % (kPair * kWarps) == 0,
+              "each stage must belong to one consumer warp");
 
-// Dims 4l .. 4l + 3 of K (side 0) or V (side 1) of a page row.
-__device__ __forceinline__ void load4(const uint8_t* page, int fmt, int g, int row, int side, int lane, float (&x)[4]) {
-  if (fmt == PBS_KV_BF16) {
-    const uint2 w = *reinterpret_cast<const uint2*>(page + (g * kPageRows + row) * 512 + side * 256 + lane * 8);
-    x[0] = bf16_lo(w.x); x[1] = bf16_hi(w.x); x[2] = bf16_lo(w.y); x[3] = bf16_hi(w.y);
-  } else if (fmt == PBS_KV_FP8_E4M3) {
-    const uint32_t w = *reinterpret_cast<const uint32_t*>(page + (g * kPageRows + row) * 256 + side * 128 + lane * 4);
-    const uint32_t a = e4m3x2_to_f16x2(w), b = e4m3x2_to_f16x2(w >> 16);
-    x[0] = half_of(a, 0); x[1] = half_of(a, 1); x[2] = half_of(b, 0); x[3] = half_of(b, 1);
-  } else {
-    const uint8_t* sl = page + (2 * g + side) * 1152;
-    const uint32_t w = *reinterpret_cast<const uint16_t*>(sl + row * 64 + lane * 2);
-    const float s = half_of(e4m3x2_to_f16x2(sl[1024 + row * 8 + (lane >> 2)]), 0);
-    const uint32_t a = e2m1x2_to_f16x2(w & 0xff), b = e2m1x2_to_f16x2(w >> 8);
-    x[0] = half_of(a, 0) * s; x[1] = half_of(a, 1) * s; x[2] = half_of(b, 0) * s; x[3] = half_of(b, 1) * s;
+template <int NT>
+struct Merge {
+  float o[kWarps][8 * NT][kOPitch];
+  float m[kWarps][8 * NT];
+  float l[kWarps][8 * NT];
+};
+
+template <int FMT>
+struct Ctl {
+  uint64_t full[kStages<FMT>];
+  uint64_t empty[kStages<FMT>];
+  int32_t ok[kStages<FMT>];  // the stage holds a page (0: padding, or a page that is not in the cache)
+  int32_t abort;
+  int32_t last;
+  int32_t item;              // where this CTA's part begins
+  int32_t warp_sums[kWarps + 1];
+  int64_t offset, total;
+};
+
+template <int FMT, int NT>
+constexpr size_t kSmem = 1024 + size_t(kStages<FMT>) * wp::kStageBytes<FMT> + sizeof(Merge<NT>) + sizeof(Ctl<FMT>);
+
+// One group of rows and its page list.
+struct Item {
+  int req, row0, rows;  // first of its rows in q, how many
+  int p0, p1;           // their positions
+  int head_pages;       // pages [0, head_pages), then
+  int first_page;       // pages first_page ..
+  int real;             // pages of the list
+  int pages;            // real, padded to pairs (one pair at least)
+};
+
+__device__ __forceinline__ void page_list(const WindowArgs& a, Item& it) {
+  it.head_pages = it.first_page = it.real = 0;
+  if (it.p1 >= 0) {
+    const int low = a.window > 0 ? max(0, max(it.p0, 0) - a.window + 1) : 0;
+    const int head = min(a.num_sinks, low);
+    it.first_page = low / kPageRows;
+    it.head_pages = min((head + kPageRows - 1) / kPageRows, it.first_page);
+    it.real = it.head_pages + it.p1 / kPageRows - it.first_page + 1;
   }
+  it.pages = max(kPair, (it.real + kPair - 1) / kPair * kPair);
 }
 
-__global__ void __launch_bounds__(kWarps * 32) window_attend_kernel(const WindowArgs a) {
-  const int row = blockIdx.x, h = blockIdx.y, g = h / a.group;
+__device__ __forceinline__ Item decode_item(const WindowArgs& a, int item) {
+  Item it;
+  it.req = item / a.groups_per_req;
+  const int r0 = (item - it.req * a.groups_per_req) * a.rows_per_group;
+  it.rows = min(a.rows_per_group, a.decode_query_len - r0);
+  it.row0 = it.req * a.decode_query_len + r0;
+  it.p0 = __ldg(a.seq_lens + it.req) - a.decode_query_len + r0;
+  it.p1 = it.p0 + it.rows - 1;
+  page_list(a, it);
+  return it;
+}
+
+// Group `item` of the prefill tokens, counting each request's groups of rows_per_group in order; rows
+// 0: there is no such group. One warp.
+__device__ __forceinline__ Item prefill_item(const WindowArgs& a, int item, int lane) {
+  Item it = {};
+  int before = 0;
+  for (int r0 = 0; r0 < a.num_reqs; r0 += 32) {
+    const int r = r0 + lane;
+    const int c0 = r < a.num_reqs ? __ldg(a.cu_seqlens_q + r) : 0;
+    const int n = r < a.num_reqs ? __ldg(a.cu_seqlens_q + r + 1) - c0 : 0;
+    const int groups = n > 0 ? (n + a.rows_per_group - 1) / a.rows_per_group : 0;
+    int incl = groups;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, incl, d);
+      if (lane >= d) incl += y;
+    }
+    const int at = item - before - (incl - groups);
+    const uint32_t hit = __ballot_sync(0xffffffffu, at >= 0 && at < groups);
+    if (hit != 0) {
+      const int src = __ffs(hit) - 1;
+      const int n_of = __shfl_sync(0xffffffffu, n, src), c_of = __shfl_sync(0xffffffffu, c0, src);
+      const int first = __shfl_sync(0xffffffffu, at, src) * a.rows_per_group;
+      it.req = r0 + src;
+      it.rows = min(a.rows_per_group, min(n_of - first, a.num_rows - c_of - first));
+      it.row0 = c_of + first;
+      it.p0 = __ldg(a.seq_lens + it.req) - n_of + first;
+      it.p1 = it.p0 + it.rows - 1;
+      if (it.rows > 0) page_list(a, it);
+      return it;
+    }
+    before += __shfl_sync(0xffffffffu, incl, 31);
+  }
+  return it;
+}
+
+// Keys n0 .. n0 + 15 that a row at position p sees, bit n - n0.
+__device__ __forceinline__ uint32_t seen_bits(const WindowArgs& a, int n0, int p) {
+  const int behind = p - n0;  // causal: bits 0 .. behind
+  if (behind < 0) return 0u;
+  uint32_t m = behind >= 15 ? 0xffffu : (2u << behind) - 1u;
+  if (a.window > 0) {
+    const int lo = p - a.window + 1 - n0;
+    const uint32_t in = lo <= 0 ? 0xffffu : lo > 15 ? 0u : (0xffffu << lo) & 0xffffu;
+    const int s = a.num_sinks - n0;
+    const uint32_t sink = s <= 0 ? 0u : s >= 16 ? 0xffffu : (1u << s) - 1u;
+    m &= in | sink;
+  }
+  return m;
+}
+
+__device__ __forceinline__ void tma_load_5d(void* dst, const void* tmap, uint64_t* bar, int c4) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %3, %3, %3, %4}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(smem_u32(bar)), "r"(0), "r"(c4)
+      : "memory");
+}
+
+__device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory"); }
+
+__device__ __forceinline__ uint16_t bf16_bits(float x) {
+  uint16_t r;
+  asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(r) : "f"(x));
+  return r;
+}
+
+// First page of part c of `parts` equal parts of `total` pages (an even number).
+__device__ __forceinline__ int64_t cut(int64_t total, int64_t c, int64_t parts) { return total / 2 * c / parts * 2; }
+
+// Output and log-sum-exp of one element, from the merged maximum, sum and O.
+__device__ __forceinline__ void store_out(const WindowArgs& a, int row, int head, int d, float M, float L, float O) {
+  const float r = L != 0.f ? a.v_scale * O / L : 0.f;  // L is 0 only without keys; NaN goes through
+  a.out[static_cast<int64_t>(row) * a.out_row_stride + static_cast<int64_t>(head) * a.out_head_stride + d] = bf16_bits(r);
+  if (a.lse != nullptr && d == 0)
+    a.lse[static_cast<int64_t>(row) * a.lse_row_stride + head] = L != 0.f ? (M + log2f(L)) * kLn2 : -INFINITY;
+}
+
+template <int FMT, bool PACKED, int NT>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm<FMT>)
+    window_attend_kernel(const __grid_constant__ CUtensorMap tmap, const WindowArgs a) {
+  constexpr int NS = kStages<FMT>;
+  constexpr int kStage = wp::kStageBytes<FMT>;
+  constexpr int kCols = 8 * NT;
+  constexpr int kSlot = kCols * (kHeadDim + 2);  // floats of a workspace partial: O, then m, then l
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* stages = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  Merge<NT>* mg = reinterpret_cast<Merge<NT>*>(stages + NS * kStage);
+  Ctl<FMT>* ctl = reinterpret_cast<Ctl<FMT>*>(mg + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  int req, pos;
-  if (a.cu_seqlens_q != nullptr) {
-    if (row >= __ldg(a.cu_seqlens_q + a.num_reqs)) return;  // behind the last request
-    prefill_position(row, a.cu_seqlens_q, a.num_reqs, a.seq_lens, req, pos);
+  const bool split = a.split_ws != nullptr;
+  const int H = a.num_kv_heads;
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < NS; ++i) {
+      mbar_init(&ctl->full[i], 1);
+      mbar_init(&ctl->empty[i], 1);
+    }
+    ctl->abort = 0;
+    fence_mbar_init();
+  }
+
+  // ---- this CTA's part of the page sequence: `left` pages from page `off` of unit (item, g)
+  int item, g;
+  int off = 0;
+  int64_t left, parts = 1, total = 0, start = 0;
+  Item it;
+  if (split) {
+    const int n_items = a.num_reqs * a.groups_per_req;
+    const int per = (n_items + kThreads - 1) / kThreads;
+    const int i0 = min(static_cast<int>(threadIdx.x) * per, n_items), i1 = min(i0 + per, n_items);
+    // pages per kv head fit 32 bits: an item has at most 2^27, so sums are kept in 64
+    int64_t mine = 0;
+    for (int i = i0; i < i1; ++i) mine += decode_item(a, i).pages;
+    int64_t incl = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int64_t y = __shfl_up_sync(0xffffffffu, incl, d);
+      if (lane >= d) incl += y;
+    }
+    __shared__ int64_t sums[kWarps + 1];
+    if (lane == 31) sums[warp] = incl;
+    __syncthreads();
+    int64_t before = incl - mine;
+    for (int w = 0; w < kWarps + 1; ++w) {
+      if (w < warp) before += sums[w];
+      total += sums[w];
+    }
+    total *= H;
+    parts = min(static_cast<int64_t>(gridDim.x), max(int64_t(1), total / a.min_pages));
+    if (blockIdx.x >= parts) return;
+    start = cut(total, blockIdx.x, parts);
+    left = cut(total, blockIdx.x + 1, parts) - start;
+    if (start >= before * H && start < (before + mine) * H) {
+      int64_t at = before * H;
+      for (int i = i0; i < i1; ++i) {
+        const int64_t w = static_cast<int64_t>(decode_item(a, i).pages) * H;
+        if (start < at + w) {
+          ctl->item = i;
+          ctl->offset = start - at;
+          break;
+        }
+        at += w;
+      }
+    }
+    __syncthreads();
+    item = ctl->item;
+    it = decode_item(a, item);
+    g = static_cast<int>(ctl->offset / it.pages);
+    off = static_cast<int>(ctl->offset % it.pages);
   } else {
-    decode_position(row, a.decode_query_len, a.seq_lens, req, pos);
+    __syncthreads();
+    item = blockIdx.x;
+    g = blockIdx.y;
+    it = a.cu_seqlens_q != nullptr ? prefill_item(a, item, lane) : decode_item(a, item);
+    if (it.rows <= 0) return;
+    left = it.pages;
   }
-  const int low = a.window > 0 ? max(0, pos - a.window + 1) : 0;
-  const int head = pos < 0 ? 0 : min(a.num_sinks, low);
-  const int count = pos < 0 ? 0 : head + pos - low + 1;
-  const uint16_t* qp = a.q + row * a.q_row_stride + h * a.q_head_stride + 4 * lane;
-  float q[4];
+
+  if (warp == kWarps) {
+    // ---------------------------------------------------------------- producer
+    int64_t s = 0;  // pages issued
+    bool go = true;
+    while (go && left > 0) {
+      const int end = static_cast<int>(min(static_cast<int64_t>(it.pages), off + left));
+      const int32_t* pt_row = a.page_table + static_cast<int64_t>(it.req) * a.pt_row_stride;
+      auto page_of = [&](int i) -> int {  // physical page of entry i of the unit's list, -1: none
+        if (i >= min(end, it.real)) return -1;
+        const int pg = i < it.head_pages ? i : it.first_page + (i - it.head_pages);
+        const int b = pg / kPagesPerBlock;
+        if (b >= a.max_blocks) {
+          set_err(a.err_word, PBS_DEVERR_BLOCK_OOB);
+          return -1;
+        }
+        const int phys = __ldg(pt_row + b);
+        const int64_t page = static_cast<int64_t>(phys) * a.block_page_stride + pg % kPagesPerBlock;
+        if (phys < 0 || page >= a.num_pages) {
+          set_err(a.err_word, PBS_DEVERR_PAGE_OOB);
+          return -1;
+        }
+        return static_cast<int>(page);
+      };
+      int next = page_of(off + lane);
+      for (int base = off; go && base < end; base += 32) {
+        const int ids = next;
+        if (base + 32 < end) next = page_of(base + 32 + lane);
+        const int n = min(32, end - base);
+        for (int j = 0; go && j < n; ++j, ++s) {
+          const int page = __shfl_sync(0xffffffffu, ids, j);
+          if (lane == 0) {
+            const int stage = static_cast<int>(s % NS);
+            if (s >= NS && !mbar_wait_bounded(&ctl->empty[stage], ((s / NS) - 1) & 1)) {
+              set_err(a.err_word, PBS_DEVERR_TIMEOUT);
+              atomicExch(&ctl->abort, 1);
+            }
+            go = *reinterpret_cast<volatile int32_t*>(&ctl->abort) == 0;
+            if (go) {
+              uint8_t* dst = stages + stage * kStage;
+              ctl->ok[stage] = page >= 0;
+              if (page < 0) {
+                mbar_arrive(&ctl->full[stage]);
+              } else {
+                mbar_arrive_expect_tx(&ctl->full[stage], kStage);
+                if (FMT != PBS_KV_NVFP4 && PACKED) {
+                  tma_load_5d(dst, &tmap, &ctl->full[stage], page * H + g);
+                } else if (FMT == PBS_KV_BF16) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) q[i] = __uint_as_float(static_cast<uint32_t>(qp[i]) << 16);
-  float m = -INFINITY, l = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
-  for (int i = warp; i < count; i += kWarps) {
-    const int n = i < head ? i : low + i - head;
-    const int b = n / kSparseBlock;
-    if (b >= a.max_blocks) {
-      set_err(a.err_word, PBS_DEVERR_BLOCK_OOB);
-      continue;
+                  for (int q = 0; q < 4; ++q) tma_load_4d(dst + q * 2048, &tmap, &ctl->full[stage], 64 * q, 0, g, page);
+                } else if (FMT == PBS_KV_FP8_E4M3) {
+#pragma unroll
+                  for (int q = 0; q < 2; ++q) tma_load_4d(dst + q * 2048, &tmap, &ctl->full[stage], 128 * q, 0, g, page);
+                } else {
+                  bulk_load(dst, a.kv_cache + static_cast<int64_t>(page) * a.page_stride_bytes + static_cast<int64_t>(g) * kStage,
+                            kStage, &ctl->full[stage]);
+                }
+              }
+            }
+          }
+          go = __shfl_sync(0xffffffffu, go, 0);
+          if (!go) break;
+        }
+      }
+      left -= end - off;
+      off = 0;
+      if (left > 0 && ++g == H) {
+        g = 0;
+        it = decode_item(a, ++item);
+      }
     }
-    const int phys = __ldg(a.page_table + req * a.pt_row_stride + b);
-    const int64_t page = static_cast<int64_t>(phys) * a.block_page_stride + n % kSparseBlock / kPageRows;
-    if (phys < 0 || page >= a.num_pages) {
-      set_err(a.err_word, PBS_DEVERR_PAGE_OOB);
-      continue;
-    }
-    const uint8_t* base = a.kv_cache + page * a.page_stride_bytes;
-    float k[4], v[4];
-    load4(base, a.kv_dtype, g, n % kPageRows, 0, lane, k);
-    load4(base, a.kv_dtype, g, n % kPageRows, 1, lane, v);
-    float s = q[0] * k[0] + q[1] * k[1] + q[2] * k[2] + q[3] * k[3];
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-    s *= a.scale_log2;
-    const float mn = fmaxf(m, s), mu = mn == -INFINITY ? 0.f : mn;
-    const float f = ex2(m - mu), p = ex2(s - mu);
-    m = mn;
-    l = l * f + p;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) o[j] = o[j] * f + p * v[j];
+    // every copy issued must land before the shared memory goes away
+    if (lane == 0)
+      for (int64_t p = s > NS ? s - NS : 0; p < s; ++p)
+        if (!mbar_wait_bounded(&ctl->full[p % NS], (p / NS) & 1)) {
+          set_err(a.err_word, PBS_DEVERR_TIMEOUT);
+          break;
+        }
+    return;
   }
-  __shared__ float sm[kWarps], sl[kWarps], so[kWarps][kHeadDim];
-  if (lane == 0) {
-    sm[warp] = m;
-    sl[warp] = l;
-  }
+
+  // ------------------------------------------------------------------ consumers
+  const int hh = lane >> 2, c = lane & 3;
+  const int G = a.group, gshift = __ffs(G) - 1;  // a power of two
+  const float sl2 = a.scale_log2;
+  int64_t s = 0;  // pages of the CTA's sequence before this unit
+  while (left > 0) {
+    const int first = off, end = static_cast<int>(min(static_cast<int64_t>(it.pages), off + left));
+    const int n = end - first;  // even
+    // Q fragments and each column's row
+    uint32_t qf[NT][8][2];
+    int row_of[NT][2];
 #pragma unroll
-  for (int j = 0; j < 4; ++j) so[warp][4 * lane + j] = o[j];
-  __syncthreads();
-  float M = -INFINITY, L = 0.f, O = 0.f;
-  const int d = threadIdx.x;
-  for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sm[w]);
-  if (M != -INFINITY)
-    for (int w = 0; w < kWarps; ++w) {
-      const float f = ex2(sm[w] - M);
-      L += f * sl[w];
-      O += f * so[w][d];
+    for (int t = 0; t < NT; ++t) {
+      const int col = 8 * t + hh;  // the B fragment's column
+      const int r = col >> gshift;
+      const bool live = r < it.rows;
+      const uint32_t* q32 = reinterpret_cast<const uint32_t*>(
+          a.q + static_cast<int64_t>(it.row0 + (live ? r : 0)) * a.q_row_stride +
+          static_cast<int64_t>(g * G + (live ? col & (G - 1) : 0)) * a.q_head_stride);
+#pragma unroll
+      for (int j = 0; j < 8; ++j)
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+          const uint32_t x = live ? __ldg(q32 + (wp::q_dim<FMT>(j, w, c) >> 1)) : 0u;
+          qf[t][j][w] = FMT == PBS_KV_BF16 ? x : bf16x2_to_f16x2(x);
+        }
+      row_of[t][0] = (8 * t + 2 * c) >> gshift;
+      row_of[t][1] = (8 * t + 2 * c + 1) >> gshift;
     }
-  const float r = L != 0.f ? a.v_scale * O / L : 0.f;
-  uint16_t bits;
-  asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(bits) : "f"(r));
-  a.out[row * a.out_row_stride + h * a.out_head_stride + d] = bits;
-  if (a.lse != nullptr && d == 0) a.lse[row * a.lse_row_stride + h] = L != 0.f ? (M + log2f(L)) * kLn2 : -INFINITY;
+    float o[NT][8][4], m[NT][2], l[NT][2];
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) o[t][i][0] = o[t][i][1] = o[t][i][2] = o[t][i][3] = 0.f;
+      m[t][0] = m[t][1] = -INFINITY;
+      l[t][0] = l[t][1] = 0.f;
+    }
+
+    // this warp's pairs of the unit: pair index (s + j) / 2 of the CTA's sequence, taken in turn
+    const int64_t pair0 = s / kPair;
+    for (int64_t pr = pair0 + ((warp - static_cast<int>(pair0 % kWarps)) + kWarps) % kWarps; pr < pair0 + n / kPair;
+         pr += kWarps) {
+      const int j = static_cast<int>(pr - pair0) * kPair;  // page of the unit's part
+      const int stage = static_cast<int>((pr * kPair) % NS);
+      const uint32_t parity = static_cast<uint32_t>((pr * kPair) / NS) & 1u;
+      uint32_t st[kPair];
+      int n0[kPair];
+      uint32_t whole = 0u;  // bit i: every row of the group sees all of page i
+      uint32_t real = 0u;
+#pragma unroll
+      for (int i = 0; i < kPair; ++i) {
+        st[i] = smem_u32(stages + (stage + i) * kStage);
+        const int e = first + j + i;
+        n0[i] = (e < it.head_pages ? e : it.first_page + (e - it.head_pages)) * kPageRows;
+        if (*reinterpret_cast<volatile int32_t*>(&ctl->abort) != 0 ||
+            !mbar_wait_bounded(&ctl->full[stage + i], parity)) {
+          set_err(a.err_word, PBS_DEVERR_TIMEOUT);
+          atomicExch(&ctl->abort, 1);
+        } else if (ctl->ok[stage + i] != 0) {
+          real |= 1u << i;
+          if (it.p0 >= n0[i] + kPageRows - 1 &&
+              (a.window == 0 || n0[i] > it.p1 - a.window || n0[i] + kPageRows <= a.num_sinks))
+            whole |= 1u << i;
+        }
+      }
+      real = __shfl_sync(0xffffffffu, real, 0) & __shfl_sync(0xffffffffu, real, 31);
+      whole = __shfl_sync(0xffffffffu, whole, 0) & real;
+
+      float sc[kPair][NT][4];
+      wp::page_scores<FMT, PACKED, kPair, NT>(st, qf, lane, sc);
+      float mx[NT][2];
+#pragma unroll
+      for (int t = 0; t < NT; ++t) mx[t][0] = mx[t][1] = -INFINITY;
+#pragma unroll
+      for (int i = 0; i < kPair; ++i) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) sc[i][t][x] *= sl2;
+        if (!((whole >> i) & 1u)) {
+#pragma unroll
+          for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+              const uint32_t b = ((real >> i) & 1u) && row_of[t][w] < it.rows ? seen_bits(a, n0[i], it.p0 + row_of[t][w]) : 0u;
+              if (!((b >> hh) & 1u)) sc[i][t][w] = -INFINITY;
+              if (!((b >> (hh + 8)) & 1u)) sc[i][t][w + 2] = -INFINITY;
+            }
+        }
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          mx[t][0] = fmaxf(mx[t][0], fmaxf(sc[i][t][0], sc[i][t][2]));
+          mx[t][1] = fmaxf(mx[t][1], fmaxf(sc[i][t][1], sc[i][t][3]));
+        }
+      }
+#pragma unroll
+      for (int d = 4; d < 32; d <<= 1)
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+          mx[t][0] = fmaxf(mx[t][0], __shfl_xor_sync(0xffffffffu, mx[t][0], d));
+          mx[t][1] = fmaxf(mx[t][1], __shfl_xor_sync(0xffffffffu, mx[t][1], d));
+        }
+      bool moved = false;
+      float al[NT][2], mu[NT][2];
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+          const bool grow = mx[t][w] > m[t][w] + kLazyLog2;
+          al[t][w] = grow ? ex2(m[t][w] - mx[t][w]) : 1.f;
+          m[t][w] = grow ? mx[t][w] : m[t][w];
+          mu[t][w] = m[t][w] == -INFINITY ? 0.f : m[t][w];
+          moved |= grow;
+        }
+#pragma unroll
+      for (int i = 0; i < kPair; ++i)
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int x = 0; x < 4; ++x) sc[i][t][x] = ex2(sc[i][t][x] - mu[t][x & 1]);
+#pragma unroll
+      for (int t = 0; t < NT; ++t)
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+          float add = 0.f;
+#pragma unroll
+          for (int i = 0; i < kPair; ++i) add += sc[i][t][w] + sc[i][t][w + 2];
+          l[t][w] = l[t][w] * al[t][w] + add;
+        }
+      if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) o[t][i][x] *= al[t][x & 1];
+      }
+#pragma unroll
+      for (int i = 0; i < kPair; ++i) {
+        if ((whole >> i) & 1u) {
+          wp::page_pv<FMT, PACKED, NT, false>(st[i], sc[i], lane, o, 1, [](int) { return 0u; }, row_of);
+        } else if ((real >> i) & 1u) {
+          uint32_t any = 0u, all = 0xffffu;
+          for (int r = 0; r < it.rows; ++r) {
+            const uint32_t b = seen_bits(a, n0[i], it.p0 + r);
+            any |= b;
+            all &= b;
+          }
+          const int p0 = it.p0;
+          wp::page_pv<FMT, PACKED, NT, true>(
+              st[i], sc[i], lane, o, any == all ? 1 : it.rows,
+              [&](int r) { return any == all ? any : seen_bits(a, n0[i], p0 + r); }, row_of);
+        }
+      }
+      __syncwarp();
+      if (lane == 0) {
+#pragma unroll
+        for (int i = 0; i < kPair; ++i) mbar_arrive(&ctl->empty[stage + i]);
+      }
+    }
+
+    // ---- the warps' partials meet
+#pragma unroll
+    for (int d = 4; d < 32; d <<= 1)
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        l[t][0] += __shfl_xor_sync(0xffffffffu, l[t][0], d);
+        l[t][1] += __shfl_xor_sync(0xffffffffu, l[t][1], d);
+      }
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+#pragma unroll
+        for (int x = 0; x < 4; ++x) mg->o[warp][8 * t + 2 * c + (x & 1)][wp::o_dim<FMT>(i, x >> 1, hh)] = o[t][i][x];
+      if (hh == 0) {
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+          mg->m[warp][8 * t + 2 * c + w] = m[t][w];
+          mg->l[warp][8 * t + 2 * c + w] = l[t][w];
+        }
+      }
+    }
+    consumers_sync();
+    const bool whole_unit = first == 0 && end == it.pages;
+    const int cols = it.rows * G;
+    const int d = threadIdx.x;  // 128 consumer threads: one dim each
+    float* part = nullptr;
+    if (!whole_unit) part = a.split_ws + (2 * static_cast<int64_t>(blockIdx.x) + (first == 0 ? 1 : 0)) * kSlot;
+    for (int col = 0; col < cols; ++col) {
+      float M = mg->m[0][col];
+#pragma unroll
+      for (int w = 1; w < kWarps; ++w) M = fmaxf(M, mg->m[w][col]);
+      float O = 0.f, L = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        // without a maximum every weight is 0 (or NaN, which has to stay)
+        const float f = M == -INFINITY ? 1.f : ex2(mg->m[w][col] - M);
+        O += f * mg->o[w][col][d];
+        L += f * mg->l[w][col];
+      }
+      if (whole_unit) {
+        store_out(a, it.row0 + (col >> gshift), g * G + (col & (G - 1)), d, M, L, O);
+      } else {
+        part[col * kHeadDim + d] = O;
+        if (d == 0) {
+          part[kCols * kHeadDim + col] = M;
+          part[kCols * (kHeadDim + 1) + col] = L;
+        }
+      }
+    }
+    if (!whole_unit) {
+      // publish, draw a ticket; the unit's last CTA merges its parts in page order
+      const int64_t u0 = start + s - first, u1 = u0 + it.pages;  // the unit's pages in the sequence
+      int64_t c0 = u0 * parts / total, c1 = (u1 - 1) * parts / total;
+      while (c0 > 0 && cut(total, c0, parts) > u0) --c0;
+      while (cut(total, c0 + 1, parts) <= u0) ++c0;
+      while (c1 > 0 && cut(total, c1, parts) >= u1) --c1;
+      while (c1 + 1 < parts && cut(total, c1 + 1, parts) < u1) ++c1;
+      const int64_t unit = static_cast<int64_t>(item) * H + g;
+      __threadfence();
+      consumers_sync();
+      if (threadIdx.x == 0) ctl->last = atomicAdd(a.split_tickets + unit, 1) == static_cast<int>(c1 - c0);
+      consumers_sync();
+      if (ctl->last) {
+        __threadfence();
+        for (int col = 0; col < cols; ++col) {
+          float M = -INFINITY;
+          for (int64_t p = c0; p <= c1; ++p)
+            M = fmaxf(M, __ldcg(a.split_ws + (2 * p + (p == c0 ? 1 : 0)) * kSlot + kCols * kHeadDim + col));
+          float O = 0.f, L = 0.f;
+          for (int64_t p = c0; p <= c1; ++p) {
+            const float* from = a.split_ws + (2 * p + (p == c0 ? 1 : 0)) * kSlot;
+            const float f = M == -INFINITY ? 1.f : ex2(__ldcg(from + kCols * kHeadDim + col) - M);
+            O += f * __ldcg(from + col * kHeadDim + d);
+            L += f * __ldcg(from + kCols * (kHeadDim + 1) + col);
+          }
+          store_out(a, it.row0 + (col >> gshift), g * G + (col & (G - 1)), d, M, L, O);
+        }
+        if (threadIdx.x == 0) a.split_tickets[unit] = 0;
+      }
+    }
+    consumers_sync();  // the merge buffer is free for the next unit
+    left -= n;
+    s += n;
+    off = 0;
+    if (left > 0 && ++g == H) {
+      g = 0;
+      it = decode_item(a, ++item);
+    }
+  }
 }
+
+template <int FMT, bool PACKED, int NT>
+cudaError_t launch_one(const WindowArgs& a, const CUtensorMap& tmap, int sms, cudaStream_t stream) {
+  constexpr size_t smem = kSmem<FMT, NT>;
+  static_assert(smem * kCtasPerSm<FMT> <= 227 * 1024, "the CTAs of an SM exceed its shared memory");
+  auto kern = window_attend_kernel<FMT, PACKED, NT>;
+  cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+  if (e != cudaSuccess) return e;
+  dim3 grid;
+  if (a.split_ws != nullptr) {
+    grid = dim3(static_cast<unsigned>(sms * kCtasPerSm<FMT>));
+  } else {
+    const int64_t groups = a.cu_seqlens_q != nullptr
+                               ? static_cast<int64_t>(a.num_rows) / a.rows_per_group + a.num_reqs
+                               : static_cast<int64_t>(a.num_reqs) * a.groups_per_req;
+    grid = dim3(static_cast<unsigned>(groups), static_cast<unsigned>(a.num_kv_heads));
+  }
+  kern<<<grid, kThreads, smem, stream>>>(tmap, a);
+  return cudaGetLastError();
+}
+
+template <int FMT, bool PACKED>
+cudaError_t launch_cols(const WindowArgs& a, const CUtensorMap& tmap, int sms, cudaStream_t stream) {
+  return a.rows_per_group * a.group > 8 ? launch_one<FMT, PACKED, 2>(a, tmap, sms, stream)
+                                        : launch_one<FMT, PACKED, 1>(a, tmap, sms, stream);
+}
+
+constexpr int kMaxCtasPerSm = 3;
+constexpr size_t kMaxPartialBytes = 16 * (kHeadDim + 2) * sizeof(float);
 
 }  // namespace
 
-cudaError_t launch_window_attend(const WindowArgs& a, cudaStream_t stream) {
-  window_attend_kernel<<<dim3(a.num_rows, a.num_heads), kWarps * 32, 0, stream>>>(a);
-  return cudaGetLastError();
+size_t window_workspace_bytes(int sms, int64_t units) {
+  return static_cast<size_t>(sms) * kMaxCtasPerSm * 2 * kMaxPartialBytes + static_cast<size_t>(units) * sizeof(int32_t);
+}
+
+void window_geometry(WindowArgs* a, int max_rows) {
+  // 8 columns while the rows at hand fit them, else 16
+  const int cols = static_cast<int64_t>(max_rows) * a->group <= 8 ? 8 : 16;
+  a->rows_per_group = max_rows < cols / a->group ? max_rows : cols / a->group;
+  a->groups_per_req = (a->decode_query_len + a->rows_per_group - 1) / a->rows_per_group;
+}
+
+cudaError_t launch_window_attend(const WindowArgs& a, const CUtensorMap& tmap, bool packed, int sms,
+                                 cudaStream_t stream) {
+  switch (a.kv_dtype) {
+    case PBS_KV_BF16:
+      return packed ? launch_cols<PBS_KV_BF16, true>(a, tmap, sms, stream)
+                    : launch_cols<PBS_KV_BF16, false>(a, tmap, sms, stream);
+    case PBS_KV_FP8_E4M3:
+      return packed ? launch_cols<PBS_KV_FP8_E4M3, true>(a, tmap, sms, stream)
+                    : launch_cols<PBS_KV_FP8_E4M3, false>(a, tmap, sms, stream);
+    case PBS_KV_NVFP4: return launch_cols<PBS_KV_NVFP4, false>(a, tmap, sms, stream);
+    default: return cudaErrorInvalidValue;
+  }
 }
 
 }  // namespace pbs

@@ -1,0 +1,257 @@
+// One 16-row page of one kv head in shared memory, for the window attend's mma.sync kernel: scores
+// S^T = K Q^T and O^T += V^T P^T with the keys as the MMA's M (scores) and K (output) dimension and
+// NT n8-tiles of query columns (a column = one query head of one row of the group).
+//
+// Stage layouts: bf16 [4 quarter rows: K lo, K hi, V lo, V hi][16 rows][128 B] and fp8 [K, V][16
+// rows][128 B], 128B-swizzled (packed caches arrive as one box of 8-row atoms, see line_off); NVFP4
+// the K slot (1152 B) and the V slot as stored.
+//
+// A lane (hh = lane / 4, c = lane % 4) holds scores of keys hh, hh + 8 in columns 2c, 2c + 1 of a
+// tile, and V^T fragments of keys 2c, 2c + 1 (first half of the MMA's k) and 2c + 8, 2c + 9.
+#pragma once
+
+#include "pbs_device.cuh"
+
+namespace pbs {
+namespace wp {
+
+template <int FMT>
+constexpr int kStageBytes = FMT == PBS_KV_BF16 ? 8192 : FMT == PBS_KV_FP8_E4M3 ? 4096 : 2304;
+constexpr int kNvfp4Slot = 1152;
+
+// Byte offset of the 128-byte line of page row r, quarter q of a bf16 row / half q of an fp8 row.
+template <int FMT, bool PACKED>
+__device__ __forceinline__ uint32_t line_off(int r, int q) {
+  if (!PACKED) return q * 2048 + r * 128;
+  if (FMT == PBS_KV_BF16) return (r >> 3) * 4096 + q * 1024 + (r & 7) * 128;
+  return (r >> 3) * 2048 + q * 1024 + (r & 7) * 128;
+}
+
+__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds16(uint32_t addr) {
+  uint16_t v;
+  asm volatile("ld.shared.b16 %0, [%1];" : "=h"(v) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ uint32_t lds8(uint32_t addr) {
+  uint16_t v;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=h"(v) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t addr) {
+  uint2 v;
+  asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ uint4 lds128(uint32_t addr) {
+  uint4 v;
+  asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
+  return v;
+}
+__device__ __forceinline__ uint32_t word_of(const uint4& v, int i) {
+  return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
+}
+
+// First of the two dims (the second is +8 for bf16, +2 otherwise) of Q fragment word w of k-step j:
+// the order in which page_scores feeds K's dims to the MMA.
+template <int FMT>
+__device__ __forceinline__ int q_dim(int j, int w, int c) {
+  if (FMT == PBS_KV_BF16) return 16 * j + 2 * c + 8 * w;
+  if (FMT == PBS_KV_FP8_E4M3) return 16 * j + 4 * c + 2 * w;
+  return 32 * c + 4 * j + 2 * w;
+}
+
+// Scores of the pages at st[0..NP): s[page][tile][..]. The pages' chains interleave.
+template <int FMT, bool PACKED, int NP, int NT>
+__device__ __forceinline__ void page_scores(const uint32_t (&st)[NP], const uint32_t (&qf)[NT][8][2], int lane,
+                                            float (&s)[NP][NT][4]) {
+  const int hh = lane >> 2, c = lane & 3;
+#pragma unroll
+  for (int i = 0; i < NP; ++i)
+#pragma unroll
+    for (int t = 0; t < NT; ++t) s[i][t][0] = s[i][t][1] = s[i][t][2] = s[i][t][3] = 0.f;
+  if (FMT == PBS_KV_BF16) {
+    const int key = (lane & 7) + ((lane >> 3) & 1) * 8;
+    const int hi = lane >> 4;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int chunk = 2 * (j & 3) + hi;
+#pragma unroll
+      for (int i = 0; i < NP; ++i) {
+        uint32_t af[4];
+        ldsm_x4(st[i] + line_off<FMT, PACKED>(key, j >> 2) + ((chunk ^ (key & 7)) << 4), af);
+#pragma unroll
+        for (int t = 0; t < NT; ++t) mma_bf16(s[i][t], af, qf[t][j][0], qf[t][j][1]);
+      }
+    }
+  } else if (FMT == PBS_KV_FP8_E4M3) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+#pragma unroll
+      for (int i = 0; i < NP; ++i) {
+        const uint32_t w0 = lds32(st[i] + line_off<FMT, PACKED>(hh, 0) + ((j ^ hh) << 4) + 4 * c);
+        const uint32_t w1 = lds32(st[i] + line_off<FMT, PACKED>(hh + 8, 0) + ((j ^ hh) << 4) + 4 * c);
+        uint32_t af[4] = {e4m3x2_to_f16x2(w0), e4m3x2_to_f16x2(w1), e4m3x2_to_f16x2(w0 >> 16),
+                          e4m3x2_to_f16x2(w1 >> 16)};
+#pragma unroll
+        for (int t = 0; t < NT; ++t) mma_f16(s[i][t], af, qf[t][j][0], qf[t][j][1]);
+      }
+    }
+  } else {
+    uint4 k0[NP], k1[NP];
+    uint32_t s0lo[NP], s0hi[NP], s1lo[NP], s1hi[NP];
+#pragma unroll
+    for (int i = 0; i < NP; ++i) {
+      k0[i] = lds128(st[i] + hh * 64 + 16 * c);
+      k1[i] = lds128(st[i] + (hh + 8) * 64 + 16 * c);
+      const uint32_t sc0 = e4m3x2_to_f16x2(lds16(st[i] + 1024 + hh * 8 + 2 * c));
+      const uint32_t sc1 = e4m3x2_to_f16x2(lds16(st[i] + 1024 + (hh + 8) * 8 + 2 * c));
+      s0lo[i] = prmt(sc0, sc0, 0x1010);
+      s0hi[i] = prmt(sc0, sc0, 0x3232);
+      s1lo[i] = prmt(sc1, sc1, 0x1010);
+      s1hi[i] = prmt(sc1, sc1, 0x3232);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+#pragma unroll
+      for (int i = 0; i < NP; ++i) {
+        const uint32_t w0 = word_of(k0[i], j >> 1) >> (16 * (j & 1));
+        const uint32_t w1 = word_of(k1[i], j >> 1) >> (16 * (j & 1));
+        const uint32_t sa = j < 4 ? s0lo[i] : s0hi[i], sb = j < 4 ? s1lo[i] : s1hi[i];
+        uint32_t af[4] = {hmul2(e2m1x2_to_f16x2(w0), sa), hmul2(e2m1x2_to_f16x2(w1), sb),
+                          hmul2(e2m1x2_to_f16x2(w0 >> 8), sa), hmul2(e2m1x2_to_f16x2(w1 >> 8), sb)};
+#pragma unroll
+        for (int t = 0; t < NT; ++t) mma_f16(s[i][t], af, qf[t][j][0], qf[t][j][1]);
+      }
+    }
+  }
+}
+
+// The 16-bit words of a V^T fragment whose keys are in `bits` (bit n = key n of the page), this
+// lane's keys only: x for the MMA's first 8 keys (2c, 2c + 1), y for the last 8.
+__device__ __forceinline__ uint2 key_words(uint32_t bits, int c) {
+  const uint32_t a = bits >> (2 * c), b = bits >> (2 * c + 8);
+  return make_uint2(((a & 1u) ? 0xffffu : 0u) | ((a & 2u) ? 0xffff0000u : 0u),
+                    ((b & 1u) ? 0xffffu : 0u) | ((b & 2u) ? 0xffff0000u : 0u));
+}
+
+// O^T += V^T P^T of one page, p[tile][..] laid out as page_scores returns it. bf16 V: P as bf16 hi +
+// lo (two MMAs: P keeps 16 bits); fp8 / NVFP4: V exact in f16, P in f16 (2^-11).
+//
+// MASKED: `bits` are the keys that every row of the group agrees to see (rows == 1), or, per row r,
+// row_bits(r); V of the other keys is cleared in registers before it meets P, since 0 * NaN is NaN.
+// When the rows differ, each row's product goes to a scratch accumulator that is added to that row's
+// columns only.
+template <int FMT, bool PACKED, int NT, bool MASKED, typename RowBits>
+__device__ __forceinline__ void page_pv(uint32_t st, const float (&p)[NT][4], int lane, float (&o)[NT][8][4],
+                                        int rows, RowBits row_bits, const int (&row_of)[NT][2]) {
+  const int hh = lane >> 2, c = lane & 3;
+  uint32_t b0[NT], b1[NT], l0[NT], l1[NT];
+#pragma unroll
+  for (int t = 0; t < NT; ++t) {
+    if (FMT == PBS_KV_BF16) {
+      const uint32_t h01 = pack_bf16(p[t][0], p[t][1]), h23 = pack_bf16(p[t][2], p[t][3]);
+      b0[t] = movmatrix_trans(h01);
+      b1[t] = movmatrix_trans(h23);
+      l0[t] = movmatrix_trans(pack_bf16(p[t][0] - bf16_lo(h01), p[t][1] - bf16_hi(h01)));
+      l1[t] = movmatrix_trans(pack_bf16(p[t][2] - bf16_lo(h23), p[t][3] - bf16_hi(h23)));
+    } else {
+      b0[t] = movmatrix_trans(pack_f16(p[t][0], p[t][1]));
+      b1[t] = movmatrix_trans(pack_f16(p[t][2], p[t][3]));
+    }
+  }
+  auto product = [&](int i, const uint32_t (&vf)[4]) {
+    if (!MASKED) {
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        if (FMT == PBS_KV_BF16) {
+          mma_bf16(o[t][i], vf, b0[t], b1[t]);
+          mma_bf16(o[t][i], vf, l0[t], l1[t]);
+        } else {
+          mma_f16(o[t][i], vf, b0[t], b1[t]);
+        }
+      }
+      return;
+    }
+#pragma unroll 1
+    for (int r = 0; r < rows; ++r) {
+      const uint2 m = key_words(row_bits(r), c);
+      const uint32_t vm[4] = {vf[0] & m.x, vf[1] & m.x, vf[2] & m.y, vf[3] & m.y};
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        float x[4] = {0.f, 0.f, 0.f, 0.f};
+        if (FMT == PBS_KV_BF16) {
+          mma_bf16(x, vm, b0[t], b1[t]);
+          mma_bf16(x, vm, l0[t], l1[t]);
+        } else {
+          mma_f16(x, vm, b0[t], b1[t]);
+        }
+        const bool y0 = rows == 1 || row_of[t][0] == r, y1 = rows == 1 || row_of[t][1] == r;
+        o[t][i][0] = y0 ? o[t][i][0] + x[0] : o[t][i][0];
+        o[t][i][1] = y1 ? o[t][i][1] + x[1] : o[t][i][1];
+        o[t][i][2] = y0 ? o[t][i][2] + x[2] : o[t][i][2];
+        o[t][i][3] = y1 ? o[t][i][3] + x[3] : o[t][i][3];
+      }
+    }
+  };
+  if (FMT == PBS_KV_BF16) {
+    const int mi = lane >> 3;
+    const int key = (lane & 7) + 8 * (mi >> 1);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int chunk = 2 * (i & 3) + (mi & 1);
+      uint32_t vf[4];
+      ldsm_x4_trans(st + line_off<FMT, PACKED>(key, 2 + (i >> 2)) + ((chunk ^ (key & 7)) << 4), vf);
+      product(i, vf);
+    }
+  } else if (FMT == PBS_KV_FP8_E4M3) {
+    const uint4 va = lds128(st + line_off<FMT, PACKED>(2 * c, 1) + ((hh ^ ((2 * c) & 7)) << 4));
+    const uint4 vb = lds128(st + line_off<FMT, PACKED>(2 * c + 1, 1) + ((hh ^ ((2 * c + 1) & 7)) << 4));
+    const uint4 vc = lds128(st + line_off<FMT, PACKED>(2 * c + 8, 1) + ((hh ^ ((2 * c + 8) & 7)) << 4));
+    const uint4 vd = lds128(st + line_off<FMT, PACKED>(2 * c + 9, 1) + ((hh ^ ((2 * c + 9) & 7)) << 4));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint32_t sel = (i & 1) ? 0x7362u : 0x5140u;
+      const uint32_t x = prmt(word_of(va, i >> 1), word_of(vb, i >> 1), sel);
+      const uint32_t y = prmt(word_of(vc, i >> 1), word_of(vd, i >> 1), sel);
+      uint32_t vf[4] = {e4m3x2_to_f16x2(x), e4m3x2_to_f16x2(x >> 16), e4m3x2_to_f16x2(y), e4m3x2_to_f16x2(y >> 16)};
+      product(i, vf);
+    }
+  } else {
+    const uint32_t vc0 = st + kNvfp4Slot, vs0 = st + kNvfp4Slot + 1024;
+    const uint2 wa = lds64(vc0 + (2 * c) * 64 + 8 * hh);
+    const uint2 wb = lds64(vc0 + (2 * c + 1) * 64 + 8 * hh);
+    const uint2 wc = lds64(vc0 + (2 * c + 8) * 64 + 8 * hh);
+    const uint2 wd = lds64(vc0 + (2 * c + 9) * 64 + 8 * hh);
+    const uint32_t sab = e4m3x2_to_f16x2(lds8(vs0 + (2 * c) * 8 + hh) | (lds8(vs0 + (2 * c + 1) * 8 + hh) << 8));
+    const uint32_t scd = e4m3x2_to_f16x2(lds8(vs0 + (2 * c + 8) * 8 + hh) | (lds8(vs0 + (2 * c + 9) * 8 + hh) << 8));
+#pragma unroll
+    for (int wh = 0; wh < 2; ++wh) {
+      const uint32_t A = wh ? wa.y : wa.x, B = wh ? wb.y : wb.x;
+      const uint32_t C = wh ? wc.y : wc.x, D = wh ? wd.y : wd.x;
+      const uint32_t lo_ab = (A & 0x0F0F0F0Fu) | ((B & 0x0F0F0F0Fu) << 4);
+      const uint32_t hi_ab = ((A >> 4) & 0x0F0F0F0Fu) | (B & 0xF0F0F0F0u);
+      const uint32_t lo_cd = (C & 0x0F0F0F0Fu) | ((D & 0x0F0F0F0Fu) << 4);
+      const uint32_t hi_cd = ((C >> 4) & 0x0F0F0F0Fu) | (D & 0xF0F0F0F0u);
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        uint32_t vf[4] = {hmul2(e2m1x2_to_f16x2(lo_ab >> (8 * b)), sab), hmul2(e2m1x2_to_f16x2(hi_ab >> (8 * b)), sab),
+                          hmul2(e2m1x2_to_f16x2(lo_cd >> (8 * b)), scd), hmul2(e2m1x2_to_f16x2(hi_cd >> (8 * b)), scd)};
+        product(4 * wh + b, vf);
+      }
+    }
+  }
+}
+
+// Output dims of accumulator words 0/1 and 2/3 of o[..][i].
+template <int FMT>
+__device__ __forceinline__ int o_dim(int i, int half, int hh) {
+  return FMT == PBS_KV_BF16 ? 16 * i + hh + 8 * half : 16 * hh + 2 * i + half;
+}
+
+}  // namespace wp
+}  // namespace pbs
