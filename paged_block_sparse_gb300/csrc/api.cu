@@ -1071,6 +1071,21 @@ int pbs_window_prefill_attention(const void* q, int64_t q_row_stride, int64_t q_
   w.num_reqs = num_reqs;
   w.num_rows = total_q;
   w.decode_query_len = 1;
+  // the tcgen05 kernel: its workspace, rows that a tensor map and 16-byte stores can address, and a
+  // positive scale (its row maximum is taken before the scale)
+  const int64_t slots = pbs::window_image_slots(total_q, num_reqs, max_blocks, window, num_sinks);
+  if (workspace != nullptr && aligned(workspace, 256) &&
+      workspace_bytes >= pbs::window_prefill_workspace(slots, num_kv_heads) && slots <= 0x7fffffff && w.scale_log2 > 0.f &&
+      aligned(q, 16) && aligned(out, 16) && q_row_stride > 0 && q_head_stride > 0 && q_row_stride % 8 == 0 &&
+      q_head_stride % 8 == 0 && out_row_stride % 8 == 0 && out_head_stride % 8 == 0) {
+    CUtensorMap q_map;
+    st = encode_q_map(&q_map, q, num_heads, w.group, total_q, q_row_stride, q_head_stride);
+    if (st != PBS_OK) return st;
+    pbs::window_attach_images(&w, workspace, slots);
+    return pbs::launch_window_prefill_tc(w, q_map, num_sms(), reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
+               ? PBS_OK
+               : PBS_ERR_CUDA;
+  }
   pbs::window_geometry(&w, 16);
   return launch_window(w, num_sms(), stream);
 }
@@ -1080,7 +1095,8 @@ size_t pbs_window_prefill_workspace_bytes(int32_t total_q, int32_t num_reqs, int
   if (total_q <= 0 || num_reqs <= 0 || num_kv_heads <= 0 || max_blocks <= 0 || window < 0 || num_sinks < 0 ||
       kv_dtype < PBS_KV_BF16 || kv_dtype > PBS_KV_NVFP4)
     return 0;
-  return 256;
+  return pbs::window_prefill_workspace(pbs::window_image_slots(total_q, num_reqs, max_blocks, window, num_sinks),
+                                       num_kv_heads);
 }
 
 // ---- K/V insert and block operations ---------------------------------------------------------

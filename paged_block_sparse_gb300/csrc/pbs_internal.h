@@ -275,6 +275,11 @@ struct WindowArgs {
   float* split_ws;          // non-null: the page sequence is cut evenly between the CTAs
   int32_t* split_tickets;   // one per (group, kv head), zero between calls
   int32_t min_pages;        // pages a CTA takes at least
+  // tcgen05 prefill: the images of the blocks its requests see, [slot][kv head], and their info words
+  uint8_t* k_images;
+  uint8_t* v_images;
+  int32_t* image_info;
+  int32_t image_slots;
 };
 
 // Sets rows_per_group and groups_per_req for requests of up to max_rows rows.
@@ -284,5 +289,12 @@ size_t window_workspace_bytes(int sms, int64_t units);
 // `tmap`: as for launch_attend (packed: the 5-D one-box-per-(page, head) map).
 cudaError_t launch_window_attend(const WindowArgs& a, const CUtensorMap& tmap, bool packed, int sms,
                                  cudaStream_t stream);
+
+// Window prefill on tcgen05 (window_prefill_tc.cu): block images a call needs at most, its workspace, and
+// the launch of its two kernels. `q_map`: the tile kernel's Q map (box {64, G, 128 / G}); scale_log2 > 0.
+int64_t window_image_slots(int64_t total_q, int64_t num_reqs, int64_t max_blocks, int64_t window, int64_t num_sinks);
+size_t window_prefill_workspace(int64_t slots, int64_t num_kv_heads);
+void window_attach_images(WindowArgs* a, void* workspace, int64_t slots);
+cudaError_t launch_window_prefill_tc(const WindowArgs& a, const CUtensorMap& q_map, int sms, cudaStream_t stream);
 
 }  // namespace pbs

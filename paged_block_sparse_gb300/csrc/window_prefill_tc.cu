@@ -1,0 +1,762 @@
+// Window attend with sinks, varlen prefill, on the 5th-generation tensor cores (tcgen05 + TMEM). For a
+// token at position p of its request, out = v_scale * softmax(softmax_scale * k_scale * q K^T) V over the
+// keys 0 <= n <= p with n > p - window (any n when window is 0) or n < num_sinks.
+//
+// 1. convert_kernel: K and V of every 128-key block that some token of its request sees, per kv head, as
+//    the 32 KiB shared-memory images of the MMA operands ([64-dim half][128 keys][128 B], 128B swizzle): K
+//    in bf16 (exact for every format), V in fp16 times 2^-e with the block's largest finite |V| at
+//    2^14..2^15 (exact: bf16 has 8 significant bits, fp16 keeps 28 binades below its largest value). It
+//    resolves the page table once, dequantises once, and clears the keys that nobody sees, so that the
+//    attend streams images with plain bulk copies. HBM-bound.
+// 2. attend: persistent, one CTA per SM. A tile is 2 T consecutive tokens of one request (T = 128 / G) and
+//    one kv head: two 128-row MMA tiles A and B (row = token * G + head) that share every K and V block, so
+//    a block is read once per 256 rows, and the tensor cores work on one while the softmax of the other
+//    runs. Bound by the tensor pipe and, next, by the softmax warps' issue slots.
+//      warp 2     schedules: the next tile's description in one of two slots
+//      warp 0     loads: the tile's Q (tensor map), K and V images through one ring of 5 stages
+//      warp 1     issues the MMAs, in the order PV_A(i-1) S_A(i) PV_B(i-1) S_B(i)
+//      warps 4-7  softmax and output of A, one thread per row; warps 8-11 of B
+//    TMEM: S_A, S_B, O_A, O_B, 128 fp32 columns each. A row's thread reads its 128 scores, writes P as fp16
+//    over the first 64 of those columns (the A operand of PV). MMAs of one thread run in issue order, so
+//    S(i + 1) may overwrite P(i) as soon as PV(i) has been issued.
+//    P is rounded to fp16 (2^-11; bf16's 2^-8 would double the error of a bf16 output), sums stay in fp32.
+//    Online softmax in base 2: the reference moves, and O is rescaled, only when the row maximum passes
+//    it by 2^8. Each row keeps the exponent E of its O (O holds sum(P V) * 2^-E); a block of exponent e
+//    enters as P * 2^(e - E), and E moves when e - E leaves [-8, 7].
+// Blocks are masked per row only where a row's border crosses them; a block that no row of A (or B) sees is
+// skipped for it.
+#include "pbs_device.cuh"
+#include "pbs_internal.h"
+#include "tc_device.cuh"
+
+namespace pbs {
+namespace {
+
+constexpr int kRows = 128;
+constexpr int kThreadsTc = 384;
+constexpr int kImage = 32768;          // bytes of one K or V image
+constexpr int kHalf = kImage / 2;      // its first 64 dims
+constexpr int kQTile = kRows * kHeadDim * 2;
+constexpr int kRing = 5;
+constexpr float kLazyLog2 = 8.0f;
+constexpr int kExpUp = 7, kExpDown = -8;
+constexpr unsigned long long kWaitNs = 100000000ull;
+// block info word: V exponent + 128 in the low byte (0: all of V is zero), valid pages in the next
+constexpr int kInfoBias = 128;
+
+// What a request needs of the cache: blocks [0, head) and [first, last].
+struct Span {
+  int head, first, count;  // count: blocks in all
+};
+
+__device__ __forceinline__ Span span_of(const WindowArgs& a, int p0, int p1) {
+  Span s = {0, 0, 0};
+  if (p1 < 0) return s;
+  const int low = a.window > 0 ? max(0, max(p0, 0) - a.window + 1) : 0;
+  const int head = min(a.num_sinks, low);
+  // blocks past the page table are left out (the images' workspace has no room for them)
+  const int end = min(p1 / kSparseBlock + 1, a.max_blocks);
+  s.first = min(low / kSparseBlock, end);
+  s.head = min((head + kSparseBlock - 1) / kSparseBlock, s.first);
+  s.count = s.head + end - s.first;
+  return s;
+}
+
+// Query tokens of request r (the padding of q does not count) and its first position.
+__device__ __forceinline__ int tokens_of(const WindowArgs& a, int r, int* c0, int* p0) {
+  *c0 = __ldg(a.cu_seqlens_q + r);
+  const int n = __ldg(a.cu_seqlens_q + r + 1) - *c0;
+  *p0 = __ldg(a.seq_lens + r) - n;
+  return max(0, min(n, a.num_rows - *c0));
+}
+
+// The request that holds entry `index` when request r has count(r) entries, in order; `at` its entry there.
+// -1: none. A whole warp.
+template <typename Count>
+__device__ __forceinline__ int find_request(const WindowArgs& a, int index, int lane, int* at, Count count) {
+  int before = 0;
+  for (int r0 = 0; r0 < a.num_reqs; r0 += 32) {
+    const int n = r0 + lane < a.num_reqs ? count(r0 + lane) : 0;
+    int incl = n;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, incl, d);
+      if (lane >= d) incl += y;
+    }
+    const int x = index - before - (incl - n);
+    const uint32_t hit = __ballot_sync(0xffffffffu, x >= 0 && x < n);
+    if (hit != 0) {
+      const int src = __ffs(hit) - 1;
+      *at = __shfl_sync(0xffffffffu, x, src);
+      return r0 + src;
+    }
+    before += __shfl_sync(0xffffffffu, incl, 31);
+  }
+  return -1;
+}
+
+__device__ __forceinline__ int blocks_of(const WindowArgs& a, int r) {
+  int c0, p0;
+  const int n = tokens_of(a, r, &c0, &p0);
+  return n > 0 ? span_of(a, p0, p0 + n - 1).count : 0;
+}
+
+__device__ __forceinline__ float exp2i(int n) {  // 2^n, 0 below fp32's normal range
+  return n < -126 ? 0.f : __uint_as_float(static_cast<uint32_t>(127 + n) << 23);
+}
+
+// ---- images ------------------------------------------------------------------------------------
+
+__device__ __forceinline__ float f16_lo(uint32_t x) {
+  float f;
+  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.f32.f16 %0, lo;\n\t}" : "=f"(f) : "r"(x));
+  return f;
+}
+__device__ __forceinline__ float f16_hi(uint32_t x) {
+  float f;
+  asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.f32.f16 %0, hi;\n\t}" : "=f"(f) : "r"(x));
+  return f;
+}
+
+// One quarter (32 dims) of a key's K or V as stored.
+template <int FMT>
+struct Quarter {
+  uint4 w[FMT == PBS_KV_BF16 ? 4 : FMT == PBS_KV_FP8_E4M3 ? 2 : 1];
+  uint32_t scales;  // NVFP4: the two e4m3 block scales
+};
+
+template <int FMT>
+__device__ __forceinline__ Quarter<FMT> load_quarter(const uint8_t* page, int g, int row, int side, int quarter) {
+  Quarter<FMT> q;
+  q.scales = 0;
+  if (FMT == PBS_KV_NVFP4) {
+    const uint8_t* sl = page + (2 * g + side) * 1152;
+    q.w[0] = __ldg(reinterpret_cast<const uint4*>(sl + row * 64) + quarter);
+    q.scales = __ldg(reinterpret_cast<const uint16_t*>(sl + 1024 + row * 8) + quarter);
+  } else {
+    constexpr int kRow = FMT == PBS_KV_BF16 ? 512 : 256;
+    constexpr int kN = FMT == PBS_KV_BF16 ? 4 : 2;
+    const uint4* p = reinterpret_cast<const uint4*>(page + (g * kPageRows + row) * kRow + side * (kRow / 2)) + quarter * kN;
+#pragma unroll
+    for (int i = 0; i < kN; ++i) q.w[i] = __ldg(p + i);
+  }
+  return q;
+}
+
+// Elements 8c .. 8c + 7 of the quarter as float (exact).
+template <int FMT>
+__device__ __forceinline__ void eight(const Quarter<FMT>& q, int c, float (&v)[8]) {
+  if (FMT == PBS_KV_BF16) {
+    const uint32_t u[4] = {q.w[c].x, q.w[c].y, q.w[c].z, q.w[c].w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = bf16_lo(u[i]);
+      v[2 * i + 1] = bf16_hi(u[i]);
+    }
+  } else if (FMT == PBS_KV_FP8_E4M3) {
+    const uint4& w = q.w[c >> 1];
+    const uint32_t lo = (c & 1) ? w.z : w.x, hi = (c & 1) ? w.w : w.y;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t h = e4m3x2_to_f16x2((i < 2 ? lo : hi) >> (16 * (i & 1)));
+      v[2 * i] = f16_lo(h);
+      v[2 * i + 1] = f16_hi(h);
+    }
+  } else {
+    const uint32_t w = c == 0 ? q.w[0].x : c == 1 ? q.w[0].y : c == 2 ? q.w[0].z : q.w[0].w;
+    const float s = f16_lo(e4m3x2_to_f16x2((q.scales >> (8 * (c >> 1))) & 0xffu));
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t h = e2m1x2_to_f16x2((w >> (8 * i)) & 0xffu);
+      v[2 * i] = f16_lo(h) * s;
+      v[2 * i + 1] = f16_hi(h) * s;
+    }
+  }
+}
+
+// CTA (slot, kv head), 512 threads: thread t converts dims 32 (t % 4) .. of key t / 4, so that a warp reads
+// whole rows of eight keys.
+template <int FMT>
+__global__ void __launch_bounds__(512) convert_kernel(const WindowArgs a) {
+  __shared__ int s_req, s_block;
+  __shared__ float s_max[16];
+  __shared__ uint32_t s_pages;
+  const int t = threadIdx.x, warp = t >> 5, lane = t & 31, g = blockIdx.y;
+  if (warp == 0) {
+    int at = 0;
+    const int r = find_request(a, blockIdx.x, lane, &at, [&](int i) { return blocks_of(a, i); });
+    if (lane == 0) {
+      s_req = r;
+      s_pages = 0;
+      if (r >= 0) {
+        int c0, p0;
+        const int n = tokens_of(a, r, &c0, &p0);
+        const Span s = span_of(a, p0, p0 + n - 1);
+        s_block = at < s.head ? at : s.first + at - s.head;
+        if (at == 0 && (p0 + n - 1) / kSparseBlock >= a.max_blocks) set_err(a.err_word, PBS_DEVERR_BLOCK_OOB);
+      }
+    }
+  }
+  __syncthreads();
+  const int r = s_req;
+  if (r < 0) return;
+  const int b = s_block, key = t >> 2, quarter = t & 3;
+  int c0, p0;
+  const int n_tok = tokens_of(a, r, &c0, &p0);
+  const int n = b * kSparseBlock + key;
+  bool live = n < p0 + n_tok && (a.window == 0 || n > max(p0, 0) - a.window || n < a.num_sinks);
+  const uint8_t* page = a.kv_cache;
+  const int phys = __ldg(a.page_table + static_cast<int64_t>(r) * a.pt_row_stride + b);
+  const int64_t p = static_cast<int64_t>(phys) * a.block_page_stride + key / kPageRows;
+  if (phys < 0 || p >= a.num_pages) {
+    if (live) set_err(a.err_word, PBS_DEVERR_PAGE_OOB);
+    live = false;
+  } else {
+    page += p * a.page_stride_bytes;
+    if (t % 64 == 0) atomicOr(&s_pages, 1u << (key / kPageRows));
+  }
+  Quarter<FMT> kq, vq;
+  if (live) {
+    kq = load_quarter<FMT>(page, g, key % kPageRows, 0, quarter);
+    vq = load_quarter<FMT>(page, g, key % kPageRows, 1, quarter);
+  }
+  const int64_t image = static_cast<int64_t>(blockIdx.x) * a.num_kv_heads + g;
+  uint8_t* kdst = a.k_images + image * kImage;
+  uint8_t* vdst = a.v_images + image * kImage;
+  float mx = 0.f;
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    float v[8] = {};
+    if (live) eight<FMT>(kq, c, v);
+    const int c16 = quarter * 4 + c;  // 16-byte chunk of the key's 256 bytes
+    *reinterpret_cast<uint4*>(kdst + (c16 >> 3) * kHalf + key * 128 + (((c16 & 7) ^ (key & 7)) << 4)) =
+        make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+    if (live) {
+      eight<FMT>(vq, c, v);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) mx = fmaxf(mx, fabsf(v[i]) < INFINITY ? fabsf(v[i]) : 0.f);  // finite ones
+    }
+  }
+#pragma unroll
+  for (int d = 1; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+  if (lane == 0) s_max[warp] = mx;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < 16; ++w) mx = fmaxf(mx, s_max[w]);
+  int e = mx > 0.f ? static_cast<int>((__float_as_uint(mx) >> 23) & 0xffu) - 127 - 14 : 0;
+  e = max(-100, min(100, e));
+  const float sc = exp2i(-e);
+#pragma unroll
+  for (int c = 0; c < 4; ++c) {
+    float v[8] = {};
+    if (live) eight<FMT>(vq, c, v);
+    const int c16 = quarter * 4 + c;
+    *reinterpret_cast<uint4*>(vdst + (c16 >> 3) * kHalf + key * 128 + (((c16 & 7) ^ (key & 7)) << 4)) =
+        make_uint4(pack_f16(v[0] * sc, v[1] * sc), pack_f16(v[2] * sc, v[3] * sc), pack_f16(v[4] * sc, v[5] * sc),
+                   pack_f16(v[6] * sc, v[7] * sc));
+  }
+  if (t == 0) a.image_info[image] = (mx > 0.f ? e + kInfoBias : 0) | (static_cast<int>(s_pages) << 8);
+}
+
+// ---- attend -------------------------------------------------------------------------------------
+
+struct Tile {
+  int end;            // no tile: the list is done
+  int g, t0, n_tok;   // kv head, first row of q, tokens
+  int p0;             // position of the first
+  int head, first, count;
+  int slot0, req_head, req_first;  // the request's first image slot, and its span: block b's slot is
+                                   // slot0 + (b < req_head ? b : req_head + b - req_first)
+};
+
+struct Ctl {
+  uint64_t q_full, q_empty;
+  uint64_t full[kRing], empty[kRing];
+  uint64_t s_full[2], p_full[2], pv_done[2];
+  uint64_t tile_full[2], tile_empty[2];
+  uint32_t tmem;
+  int32_t abort;
+  Tile tile[2];
+};
+
+constexpr size_t kSmemTc = 2 * kQTile + kRing * kImage + sizeof(Ctl);
+static_assert(kSmemTc <= 232448, "shared memory exceeds 227 KiB");
+constexpr uint32_t kTileUsers = 2 + 8;
+
+__device__ __forceinline__ bool wait_on(uint64_t* bar, uint32_t parity, Ctl* ctl, int32_t* err) {
+  if (mbar_wait_bounded(bar, parity, kWaitNs)) return true;
+  set_err(err, PBS_DEVERR_TIMEOUT);
+  atomicExch(&ctl->abort, 1);
+  return false;
+}
+__device__ __forceinline__ bool warp_wait_on(uint64_t* bar, uint32_t parity, Ctl* ctl, int32_t* err) {
+  return __all_sync(0xffffffffu, wait_on(bar, parity, ctl, err));
+}
+__device__ __forceinline__ bool aborted(Ctl* ctl) { return *reinterpret_cast<volatile int32_t*>(&ctl->abort) != 0; }
+
+__device__ __forceinline__ void tma_load_3d(void* dst, const void* tmap, uint64_t* bar, int c0, int c1, int c2) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2)
+      : "memory");
+}
+
+// The i-th block of a tile's list.
+__device__ __forceinline__ int tile_block(const Tile& t, int i) { return i < t.head ? i : t.first + i - t.head; }
+
+// Positions of the first and last live token of MMA tile x (0: A, 1: B); last < first: none.
+template <int kG>
+__device__ __forceinline__ void tile_rows(const Tile& t, int x, int* pa, int* pb) {
+  constexpr int T = kRows / kG;
+  *pa = t.p0 + x * T;
+  *pb = t.p0 + min(t.n_tok, (x + 1) * T) - 1;
+}
+
+// Does some row at positions pa .. pb see a key of the block at n0?
+__device__ __forceinline__ bool block_seen(const WindowArgs& a, int n0, int pa, int pb) {
+  return pb >= pa && n0 <= pb && (a.window == 0 || n0 + kSparseBlock - 1 > max(pa, 0) - a.window || n0 < a.num_sinks);
+}
+
+__device__ __forceinline__ float2 fma2(float2 x, float2 y, float2 z) {
+  float2 r;
+  asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+      "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y), "f"(z.x), "f"(z.y));
+  return r;
+}
+__device__ __forceinline__ float2 add2(float2 x, float2 y) {
+  float2 r;
+  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tadd.rn.f32x2 d, a, b;\n\t"
+      "mov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y));
+  return r;
+}
+
+template <int kG>
+__global__ void __launch_bounds__(kThreadsTc, 1)
+    prefill_kernel(const __grid_constant__ CUtensorMap q_map, const WindowArgs a) {
+  constexpr int T = kRows / kG;
+  extern __shared__ __align__(1024) uint8_t smem[];
+  if ((smem_u32(smem) & 1023u) != 0) {  // the swizzled operands need it
+    if (threadIdx.x == 0 && blockIdx.x == 0) set_err(a.err_word, PBS_DEVERR_TIMEOUT);
+    return;
+  }
+  uint8_t* q_s = smem;
+  uint8_t* ring = smem + 2 * kQTile;
+  Ctl* ctl = reinterpret_cast<Ctl*>(ring + kRing * kImage);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    ctl->abort = 0;
+    mbar_init(&ctl->q_full, 1);
+    mbar_init(&ctl->q_empty, 1);
+    for (int i = 0; i < kRing; ++i) {
+      mbar_init(&ctl->full[i], 1);
+      mbar_init(&ctl->empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&ctl->s_full[i], 1);
+      mbar_init(&ctl->p_full[i], 4);
+      mbar_init(&ctl->pv_done[i], 1);
+      mbar_init(&ctl->tile_full[i], 1);
+      mbar_init(&ctl->tile_empty[i], kTileUsers);
+    }
+    fence_mbar_init();
+  }
+  if (warp == 2) tc::alloc(&ctl->tmem, 512);
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  const uint32_t tmem = ctl->tmem;  // S_A, S_B, O_A, O_B
+
+  if (warp == 2) {
+    // ------------------------------------------------------------------ scheduler
+    int total = 0;  // request tiles
+    for (int r0 = 0; r0 < a.num_reqs; r0 += 32) {
+      int c0, p0;
+      const int n = r0 + lane < a.num_reqs ? tokens_of(a, r0 + lane, &c0, &p0) : 0;
+      total += __reduce_add_sync(0xffffffffu, static_cast<uint32_t>((n + 2 * T - 1) / (2 * T)));
+    }
+    const int flat = total * a.num_kv_heads;
+    for (int k = 0;; ++k) {
+      // rounds of gridDim.x tiles, from the end (a request's last tiles see the most keys), dealt in
+      // alternating directions
+      const int f = k * static_cast<int>(gridDim.x) + static_cast<int>((k & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+      bool go = true;
+      if (lane == 0 && k >= 2) go = wait_on(&ctl->tile_empty[k & 1], ((k >> 1) - 1) & 1, ctl, a.err_word);
+      go = __shfl_sync(0xffffffffu, go && !aborted(ctl), 0);
+      Tile* t = &ctl->tile[k & 1];
+      const bool last = !go || f >= flat;
+      if (!last) {
+        int at = 0;
+        const int r = find_request(a, total - 1 - f / a.num_kv_heads, lane, &at, [&](int i) {
+          int c0, p0;
+          return (tokens_of(a, i, &c0, &p0) + 2 * T - 1) / (2 * T);
+        });
+        int slot0 = 0;
+        for (int r0 = 0; r0 < r; r0 += 32)
+          slot0 += __reduce_add_sync(0xffffffffu, static_cast<uint32_t>(r0 + lane < r ? blocks_of(a, r0 + lane) : 0));
+        if (lane == 0) {
+          int c0, p0;
+          const int n = tokens_of(a, r, &c0, &p0);
+          const Span whole = span_of(a, p0, p0 + n - 1);
+          t->g = f % a.num_kv_heads;
+          t->t0 = c0 + at * 2 * T;
+          t->n_tok = min(2 * T, n - at * 2 * T);
+          t->p0 = p0 + at * 2 * T;
+          const Span s = span_of(a, t->p0, t->p0 + t->n_tok - 1);
+          t->head = s.head;
+          t->first = s.first;
+          t->count = s.count;
+          t->slot0 = slot0;
+          t->req_head = whole.head;
+          t->req_first = whole.first;
+        }
+      }
+      if (lane == 0) {
+        t->end = last;
+        mbar_arrive(&ctl->tile_full[k & 1]);
+      }
+      __syncwarp();
+      if (last) break;
+    }
+  } else if (warp == 0) {
+    // ------------------------------------------------------------------ loads
+    if (lane == 0) {
+      asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&q_map)) : "memory");
+      int n = 0;  // images issued
+      bool go = true;
+      for (int k = 0; go; ++k) {
+        if (!wait_on(&ctl->tile_full[k & 1], (k >> 1) & 1, ctl, a.err_word)) break;
+        const Tile t = ctl->tile[k & 1];
+        mbar_arrive(&ctl->tile_empty[k & 1]);
+        if (t.end) break;
+        if (k > 0 && !wait_on(&ctl->q_empty, (k - 1) & 1, ctl, a.err_word)) break;
+        const bool two = t.n_tok > T;
+        mbar_arrive_expect_tx(&ctl->q_full, two ? 2 * kQTile : kQTile);
+        for (int x = 0; x < (two ? 2 : 1); ++x) {
+          tma_load_3d(q_s + x * kQTile, &q_map, &ctl->q_full, 0, t.g * kG, t.t0 + x * T);
+          tma_load_3d(q_s + x * kQTile + kHalf, &q_map, &ctl->q_full, 64, t.g * kG, t.t0 + x * T);
+        }
+        for (int i = 0; go && i < t.count; ++i) {
+          const int b = tile_block(t, i);
+          const int64_t image =
+              static_cast<int64_t>(t.slot0 + (b < t.req_head ? b : t.req_head + b - t.req_first)) * a.num_kv_heads + t.g;
+          for (int side = 0; side < 2; ++side, ++n) {
+            const int st = n % kRing;
+            if (n >= kRing && !wait_on(&ctl->empty[st], ((n / kRing) - 1) & 1, ctl, a.err_word)) go = false;
+            if (!go || aborted(ctl)) {
+              go = false;
+              break;
+            }
+            mbar_arrive_expect_tx(&ctl->full[st], kImage);
+            bulk_load(ring + st * kImage, (side ? a.v_images : a.k_images) + image * kImage, kImage, &ctl->full[st]);
+          }
+        }
+      }
+      // every copy must land before the CTA exits
+      for (int i = max(0, n - kRing); i < n; ++i)
+        if (!mbar_wait_bounded(&ctl->full[i % kRing], (i / kRing) & 1, kWaitNs)) set_err(a.err_word, PBS_DEVERR_TIMEOUT);
+    }
+  } else if (warp == 1) {
+    // ------------------------------------------------------------------ MMAs
+    if (lane == 0) {
+      constexpr uint32_t kIdescS = tc::idesc_f16(128, 128, true, false, false);
+      constexpr uint32_t kIdescPV = tc::idesc_f16(128, 128, false, false, true);
+      int n = 0;               // ring entries of the tiles before
+      int issued[2] = {0, 0};  // S of A, of B, over the CTA's tiles
+      int done[2] = {0, 0};    // PV
+      bool ok = true;
+      // O_x += P_x V, V in ring stage st
+      auto pv = [&](int x, int st, bool fresh) {
+        if (!wait_on(&ctl->p_full[x], done[x] & 1, ctl, a.err_word)) return false;
+        tc::fence_after_sync();
+        const uint32_t v = smem_u32(ring + st * kImage);
+#pragma unroll
+        for (int ks = 0; ks < 8; ++ks)
+          tc::mma_ts(tmem + 256 + x * 128, tmem + x * 128 + ks * 8, tc::smem_desc_sw128(v + ks * 2048, kHalf, 1024),
+                     kIdescPV, !(fresh && ks == 0));
+        tc::commit(&ctl->pv_done[x]);
+        ++done[x];
+        return true;
+      };
+      for (int k = 0; ok; ++k) {
+        if (!wait_on(&ctl->tile_full[k & 1], (k >> 1) & 1, ctl, a.err_word)) break;
+        const Tile t = ctl->tile[k & 1];
+        mbar_arrive(&ctl->tile_empty[k & 1]);
+        if (t.end) break;
+        if (!wait_on(&ctl->q_full, k & 1, ctl, a.err_word)) break;
+        int pa[2], pb[2];
+        tile_rows<kG>(t, 0, &pa[0], &pb[0]);
+        tile_rows<kG>(t, 1, &pa[1], &pb[1]);
+        bool pending[2] = {false, false}, fresh[2] = {true, true};
+        // step i: PV of block i - 1, S of block i; ring entries n + 2 i: K(i), n + 2 i + 1: V(i)
+        for (int i = 0; ok && i <= t.count; ++i) {
+          const int nk = n + 2 * i, nv = nk - 1;
+          const bool has_s = i < t.count, has_pv = i > 0;
+          if (has_pv && !wait_on(&ctl->full[nv % kRing], (nv / kRing) & 1, ctl, a.err_word)) ok = false;
+          if (ok && has_s && !wait_on(&ctl->full[nk % kRing], (nk / kRing) & 1, ctl, a.err_word)) ok = false;
+          if (!ok) break;
+          tc::fence_after_sync();
+          const int n0 = has_s ? tile_block(t, i) * kSparseBlock : 0;
+          for (int x = 0; ok && x < 2; ++x) {
+            if (pending[x]) {
+              ok = pv(x, nv % kRing, fresh[x]);
+              fresh[x] = false;
+              pending[x] = false;
+            }
+            if (ok && has_s && block_seen(a, n0, pa[x], pb[x])) {
+              const uint32_t q = smem_u32(q_s + x * kQTile), kk = smem_u32(ring + nk % kRing * kImage);
+#pragma unroll
+              for (int ks = 0; ks < 8; ++ks)
+                tc::mma_ss(tmem + x * 128, tc::smem_desc_sw128(q + (ks >> 2) * kHalf + (ks & 3) * 32, 16, 1024),
+                           tc::smem_desc_sw128(kk + (ks >> 2) * kHalf + (ks & 3) * 32, 16, 1024), kIdescS, ks > 0);
+              tc::commit(&ctl->s_full[x]);
+              ++issued[x];
+              pending[x] = true;
+            }
+          }
+          if (has_pv) tc::commit(&ctl->empty[nv % kRing]);
+          if (has_s) tc::commit(&ctl->empty[nk % kRing]);
+          if (i == t.count - 1) tc::commit(&ctl->q_empty);  // the tile's last S
+        }
+        n += 2 * t.count;
+        if (t.count == 0) tc::commit(&ctl->q_empty);
+      }
+      // every MMA must complete before TMEM is released
+      for (int x = 0; x < 2; ++x) {
+        if (done[x] > 0) mbar_wait_bounded(&ctl->pv_done[x], (done[x] - 1) & 1, kWaitNs);
+        if (issued[x] > done[x]) mbar_wait_bounded(&ctl->s_full[x], (issued[x] - 1) & 1, kWaitNs);
+      }
+    }
+  } else if (warp >= 4) {
+    // ------------------------------------------------------------------ softmax and output
+    const int x = (warp - 4) >> 2, quad = warp & 3;
+    const int row = quad * 32 + lane;
+    const int tok = row / kG, h = row % kG;
+    const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
+    const uint32_t ts = tmem + x * 128 + lane_off, to = tmem + 256 + x * 128 + lane_off;
+    const float sl2 = a.scale_log2;
+    int ns = 0;  // blocks of this MMA tile so far
+    bool ok = true;
+    for (int k = 0; ok; ++k) {
+      if (!warp_wait_on(&ctl->tile_full[k & 1], (k >> 1) & 1, ctl, a.err_word)) break;
+      const Tile t = ctl->tile[k & 1];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl->tile_empty[k & 1]);
+      if (t.end || aborted(ctl)) break;
+      int pa, pb;
+      tile_rows<kG>(t, x, &pa, &pb);
+      const bool live = x * T + tok < t.n_tok;
+      const int p = pa + tok;
+      float m = -INFINITY, l = 0.f;
+      int E = 0;
+      bool started = false;  // the tile has had a block: O holds something
+      for (int i = 0; i < t.count; ++i) {
+        const int b = tile_block(t, i), n0 = b * kSparseBlock;
+        if (!block_seen(a, n0, pa, pb)) continue;
+        const int info = __ldg(a.image_info + static_cast<int64_t>(t.slot0 + (b < t.req_head ? b : t.req_head + b - t.req_first)) *
+                                                  a.num_kv_heads + t.g);
+        const bool whole = (info >> 8) == 0xff && n0 + kSparseBlock - 1 <= pa &&
+                           (a.window == 0 || n0 > pb - a.window || n0 + kSparseBlock <= a.num_sinks);
+        if (!warp_wait_on(&ctl->s_full[x], ns & 1, ctl, a.err_word)) {
+          ok = false;
+          break;
+        }
+        tc::fence_after_sync();
+        uint32_t v[128];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tc::ld32(ts + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(&v[32 * c]));
+        tc::wait_ld();
+        bool any = live;  // does this row see a key of the block
+        if (!whole) {
+          uint32_t bits[4];
+          any = false;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            // keys 32c .. 32c + 31 of the block
+            const int base = n0 + 32 * c, behind = p - base;
+            uint32_t w = !live || behind < 0 ? 0u : behind >= 31 ? 0xffffffffu : (2u << behind) - 1u;
+            if (a.window > 0) {
+              const int lo = p - a.window + 1 - base, s = a.num_sinks - base;
+              const uint32_t in = lo <= 0 ? 0xffffffffu : lo > 31 ? 0u : 0xffffffffu << lo;
+              const uint32_t sink = s <= 0 ? 0u : s >= 32 ? 0xffffffffu : (1u << s) - 1u;
+              w &= in | sink;
+            }
+            w &= (((info >> (8 + 2 * c)) & 1) ? 0xffffu : 0u) | (((info >> (9 + 2 * c)) & 1) ? 0xffff0000u : 0u);
+            bits[c] = w;
+            any |= w != 0u;
+          }
+#pragma unroll
+          for (int j = 0; j < 128; ++j)
+            if (!(bits[j >> 5] & (1u << (j & 31)))) v[j] = 0xff800000u;  // -inf
+        }
+        float mx0 = __uint_as_float(v[0]), mx1 = __uint_as_float(v[1]);
+#pragma unroll
+        for (int j = 2; j < 128; j += 2) {
+          mx0 = fmaxf(mx0, __uint_as_float(v[j]));
+          mx1 = fmaxf(mx1, __uint_as_float(v[j + 1]));
+        }
+        const float mxs = fmaxf(mx0, mx1) * sl2;  // sl2 > 0
+        // move the reference and the exponent, rescale O
+        float f = 1.f;
+        if (any && mxs > m + kLazyLog2) {
+          f = ex2(m - mxs);  // 0 on the row's first keys
+          l *= f;
+          m = mxs;
+        }
+        const int e = info & 0xff;
+        int de = 0;
+        if (any && e != 0) {
+          de = e - kInfoBias - E;
+          if (!started || (de > kExpUp || (de < kExpDown && de >= -100))) {
+            if (started) f *= exp2i(-de);
+            E += de;
+            de = 0;
+          }
+          de = max(de, -60);  // V that far below O adds nothing; the row sum still counts its keys
+        }
+        if (__any_sync(0xffffffffu, f != 1.f)) {
+          if (ns > 0 && !warp_wait_on(&ctl->pv_done[x], (ns - 1) & 1, ctl, a.err_word)) {
+            ok = false;
+            break;
+          }
+          tc::fence_after_sync();
+          if (started) {
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              uint32_t o[32];
+              tc::ld32(to + 32 * c, o);
+              tc::wait_ld();
+#pragma unroll
+              for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+              tc::st32(to + 32 * c, o);
+            }
+          }
+        }
+        // P * 2^de, and the row sum
+        const float mu = (m == -INFINITY ? 0.f : m) - static_cast<float>(de);
+        float2 sum0 = make_float2(0.f, 0.f), sum1 = make_float2(0.f, 0.f);
+        const float2 sc = make_float2(sl2, sl2), off = make_float2(-mu, -mu);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const int i0 = 32 * c + 2 * j;
+            float2 z = fma2(make_float2(__uint_as_float(v[i0]), __uint_as_float(v[i0 + 1])), sc, off);
+            z.x = ex2(z.x);
+            z.y = ex2(z.y);
+            if (j & 1) sum1 = add2(sum1, z);
+            else sum0 = add2(sum0, z);
+            pk[j] = pack_f16(z.x, z.y);
+          }
+          tc::st16(ts + 16 * c, pk);
+        }
+        l += (sum0.x + sum0.y + sum1.x + sum1.y) * exp2i(-de);
+        started = true;
+        tc::wait_st();
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl->p_full[x]);
+        ++ns;
+      }
+      if (!ok) break;
+      // ---- output
+      const bool blocks = __any_sync(0xffffffffu, started);
+      if (blocks && !warp_wait_on(&ctl->pv_done[x], (ns - 1) & 1, ctl, a.err_word)) break;
+      tc::fence_after_sync();
+      // O * 2^E * v_scale / l, in two steps so that no factor leaves fp32's range on its own
+      const float inv = l != 0.f ? a.v_scale / l : 0.f;
+      const float f1 = exp2i(E / 2), f2 = exp2i(E - E / 2);
+      uint16_t* dst = a.out + static_cast<int64_t>(t.t0 + x * T + tok) * a.out_row_stride +
+                      static_cast<int64_t>(t.g * kG + h) * a.out_head_stride;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint32_t o[32];
+        if (blocks) {
+          tc::ld32(to + 32 * c, o);
+          tc::wait_ld();
+        }
+        if (live) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            uint32_t w[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float y0 = __uint_as_float(o[8 * q + 2 * j]) * inv * f1 * f2;
+              const float y1 = __uint_as_float(o[8 * q + 2 * j + 1]) * inv * f1 * f2;
+              w[j] = l != 0.f ? pack_bf16(y0, y1) : 0u;  // no key: O was never written, or holds zeros
+            }
+            *reinterpret_cast<uint4*>(dst + 32 * c + 8 * q) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+      }
+      if (live && a.lse != nullptr)
+        a.lse[static_cast<int64_t>(t.t0 + x * T + tok) * a.lse_row_stride + t.g * kG + h] =
+            l != 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+      tc::fence_before_sync();
+    }
+  }
+  tc::fence_before_sync();
+  __syncthreads();
+  tc::fence_after_sync();
+  if (warp == 2) tc::dealloc(tmem, 512);
+}
+
+template <int kG>
+cudaError_t launch_g(const WindowArgs& a, const CUtensorMap& q_map, int sms, cudaStream_t stream) {
+  auto kern = prefill_kernel<kG>;
+  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(kSmemTc));
+  if (e != cudaSuccess) return e;
+  const int64_t tiles = (static_cast<int64_t>(a.num_rows) / (2 * kRows / kG) + a.num_reqs) * a.num_kv_heads;
+  kern<<<static_cast<unsigned>(tiles < sms ? tiles : sms), kThreadsTc, kSmemTc, stream>>>(q_map, a);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+int64_t window_image_slots(int64_t total_q, int64_t num_reqs, int64_t max_blocks, int64_t window, int64_t num_sinks) {
+  // a request's span: its tokens' and the window's blocks with a border block at each end, and the sinks'
+  const int64_t per_token = total_q / kSparseBlock;
+  const int64_t rest = (window + kSparseBlock - 1) / kSparseBlock + 2 + (num_sinks + kSparseBlock - 1) / kSparseBlock;
+  const int64_t by_window = per_token + num_reqs * rest, by_table = num_reqs * max_blocks;
+  return window > 0 && by_window < by_table ? by_window : by_table;
+}
+
+size_t window_prefill_workspace(int64_t slots, int64_t num_kv_heads) {
+  const int64_t images = slots * num_kv_heads;
+  return static_cast<size_t>(images) * 2 * kImage + static_cast<size_t>((images * 4 + 255) / 256 * 256);
+}
+
+void window_attach_images(WindowArgs* a, void* workspace, int64_t slots) {
+  const int64_t images = slots * a->num_kv_heads;
+  a->image_slots = static_cast<int32_t>(slots);
+  a->k_images = static_cast<uint8_t*>(workspace);
+  a->v_images = a->k_images + images * kImage;
+  a->image_info = reinterpret_cast<int32_t*>(a->v_images + images * kImage);
+}
+
+cudaError_t launch_window_prefill_tc(const WindowArgs& a, const CUtensorMap& q_map, int sms, cudaStream_t stream) {
+  const dim3 grid(static_cast<unsigned>(a.image_slots), static_cast<unsigned>(a.num_kv_heads));
+  switch (a.kv_dtype) {
+    case PBS_KV_BF16: convert_kernel<PBS_KV_BF16><<<grid, 512, 0, stream>>>(a); break;
+    case PBS_KV_FP8_E4M3: convert_kernel<PBS_KV_FP8_E4M3><<<grid, 512, 0, stream>>>(a); break;
+    case PBS_KV_NVFP4: convert_kernel<PBS_KV_NVFP4><<<grid, 512, 0, stream>>>(a); break;
+    default: return cudaErrorInvalidValue;
+  }
+  const cudaError_t e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  switch (a.group) {
+    case 1: return launch_g<1>(a, q_map, sms, stream);
+    case 2: return launch_g<2>(a, q_map, sms, stream);
+    case 4: return launch_g<4>(a, q_map, sms, stream);
+    case 8: return launch_g<8>(a, q_map, sms, stream);
+    case 16: return launch_g<16>(a, q_map, sms, stream);
+    default: return cudaErrorInvalidValue;
+  }
+}
+
+}  // namespace pbs
