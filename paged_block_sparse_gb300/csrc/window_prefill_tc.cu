@@ -335,6 +335,17 @@ __device__ __forceinline__ float2 add2(float2 x, float2 y) {
   return r;
 }
 
+// 32 lanes x 16 consecutive TMEM columns.
+__device__ __forceinline__ void ld16(uint32_t taddr, uint32_t (&v)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, "
+      "[%16];"
+      : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]), "=r"(v[8]),
+        "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
+      : "r"(taddr)
+      : "memory");
+}
+
 template <int kG>
 __global__ void __launch_bounds__(kThreadsTc, 1)
     prefill_kernel(const __grid_constant__ CUtensorMap q_map, const WindowArgs a) {
@@ -371,6 +382,182 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
   tc::fence_after_sync();
   const uint32_t tmem = ctl->tmem;  // S_A, S_B, O_A, O_B
 
+  // the softmax warps hold a row's 128 scores in registers: 128 x 72 + 256 x 216 = the launch's 384 x 168
+  if (warp >= 4) {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+    // ------------------------------------------------------------------ softmax and output
+    const int x = (warp - 4) >> 2, quad = warp & 3;
+    const int row = quad * 32 + lane;
+    const int tok = row / kG, h = row % kG;
+    const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
+    const uint32_t ts = tmem + x * 128 + lane_off, to = tmem + 256 + x * 128 + lane_off;
+    const float sl2 = a.scale_log2;
+    int ns = 0;  // blocks of this MMA tile so far
+    bool ok = true;
+    for (int k = 0; ok; ++k) {
+      if (!warp_wait_on(&ctl->tile_full[k & 1], (k >> 1) & 1, ctl, a.err_word)) break;
+      const Tile t = ctl->tile[k & 1];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ctl->tile_empty[k & 1]);
+      if (t.end || aborted(ctl)) break;
+      int pa, pb;
+      tile_rows<kG>(t, x, &pa, &pb);
+      const bool live = x * T + tok < t.n_tok;
+      const int p = pa + tok;
+      float m = -INFINITY, l = 0.f;
+      int E = 0;
+      bool started = false;  // the tile has had a block: O holds something
+      for (int i = 0; i < t.count; ++i) {
+        const int b = tile_block(t, i), n0 = b * kSparseBlock;
+        if (!block_seen(a, n0, pa, pb)) continue;
+        const int info = __ldg(a.image_info + static_cast<int64_t>(t.slot0 + (b < t.req_head ? b : t.req_head + b - t.req_first)) *
+                                                  a.num_kv_heads + t.g);
+        const bool whole = (info >> 8) == 0xff && n0 + kSparseBlock - 1 <= pa &&
+                           (a.window == 0 || n0 > pb - a.window || n0 + kSparseBlock <= a.num_sinks);
+        if (!warp_wait_on(&ctl->s_full[x], ns & 1, ctl, a.err_word)) {
+          ok = false;
+          break;
+        }
+        tc::fence_after_sync();
+        uint32_t v[128];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tc::ld32(ts + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(&v[32 * c]));
+        tc::wait_ld();
+        bool any = live;  // does this row see a key of the block
+        if (!whole) {
+          uint32_t bits[4];
+          any = false;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            // keys 32c .. 32c + 31 of the block
+            const int base = n0 + 32 * c, behind = p - base;
+            uint32_t w = !live || behind < 0 ? 0u : behind >= 31 ? 0xffffffffu : (2u << behind) - 1u;
+            if (a.window > 0) {
+              const int lo = p - a.window + 1 - base, s = a.num_sinks - base;
+              const uint32_t in = lo <= 0 ? 0xffffffffu : lo > 31 ? 0u : 0xffffffffu << lo;
+              const uint32_t sink = s <= 0 ? 0u : s >= 32 ? 0xffffffffu : (1u << s) - 1u;
+              w &= in | sink;
+            }
+            w &= (((info >> (8 + 2 * c)) & 1) ? 0xffffu : 0u) | (((info >> (9 + 2 * c)) & 1) ? 0xffff0000u : 0u);
+            bits[c] = w;
+            any |= w != 0u;
+          }
+#pragma unroll
+          for (int j = 0; j < 128; ++j)
+            if (!(bits[j >> 5] & (1u << (j & 31)))) v[j] = 0xff800000u;  // -inf
+        }
+        float mx[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) mx[j] = __uint_as_float(v[j]);
+#pragma unroll
+        for (int j = 4; j < 124; j += 8)
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            mx[q] = fmaxf(mx[q], fmaxf(__uint_as_float(v[j + 2 * q]), __uint_as_float(v[j + 2 * q + 1])));
+#pragma unroll
+        for (int j = 124; j < 128; ++j) mx[j - 124] = fmaxf(mx[j - 124], __uint_as_float(v[j]));
+        const float mxs = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * sl2;  // sl2 > 0
+        // move the reference and the exponent, rescale O
+        float f = 1.f;
+        if (any && mxs > m + kLazyLog2) {
+          f = ex2(m - mxs);  // 0 on the row's first keys
+          l *= f;
+          m = mxs;
+        }
+        const int e = info & 0xff;
+        int de = 0;
+        if (any && e != 0) {
+          de = e - kInfoBias - E;
+          if (!started || (de > kExpUp || (de < kExpDown && de >= -100))) {
+            if (started) f *= exp2i(-de);
+            E += de;
+            de = 0;
+          }
+          de = max(de, -60);  // V that far below O adds nothing; the row sum still counts its keys
+        }
+        if (__any_sync(0xffffffffu, f != 1.f)) {
+          if (ns > 0 && !warp_wait_on(&ctl->pv_done[x], (ns - 1) & 1, ctl, a.err_word)) {
+            ok = false;
+            break;
+          }
+          tc::fence_after_sync();
+          if (started) {
+#pragma unroll 1
+            for (int c = 0; c < 128; c += 16) {  // few registers: the scores stay in theirs
+              uint32_t o[16];
+              ld16(to + c, o);
+              tc::wait_ld();
+#pragma unroll
+              for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
+              tc::st16(to + c, o);
+            }
+          }
+        }
+        // P * 2^de, and the row sum
+        const float mu = (m == -INFINITY ? 0.f : m) - static_cast<float>(de);
+        float2 sum0 = make_float2(0.f, 0.f), sum1 = make_float2(0.f, 0.f);
+        const float2 sc = make_float2(sl2, sl2), off = make_float2(-mu, -mu);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int j = 0; j < 16; ++j) {
+            const int i0 = 32 * c + 2 * j;
+            float2 z = fma2(make_float2(__uint_as_float(v[i0]), __uint_as_float(v[i0 + 1])), sc, off);
+            z.x = ex2(z.x);
+            z.y = ex2(z.y);
+            if (j & 1) sum1 = add2(sum1, z);
+            else sum0 = add2(sum0, z);
+            pk[j] = pack_f16(z.x, z.y);
+          }
+          tc::st16(ts + 16 * c, pk);
+        }
+        l += (sum0.x + sum0.y + sum1.x + sum1.y) * exp2i(-de);
+        started = true;
+        tc::wait_st();
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&ctl->p_full[x]);
+        ++ns;
+      }
+      if (!ok) break;
+      // ---- output
+      const bool blocks = __any_sync(0xffffffffu, started);
+      if (blocks && !warp_wait_on(&ctl->pv_done[x], (ns - 1) & 1, ctl, a.err_word)) break;
+      tc::fence_after_sync();
+      // O * 2^E * v_scale / l, in two steps so that no factor leaves fp32's range on its own
+      const float inv = l != 0.f ? a.v_scale / l : 0.f;
+      const float f1 = exp2i(E / 2), f2 = exp2i(E - E / 2);
+      uint16_t* dst = a.out + static_cast<int64_t>(t.t0 + x * T + tok) * a.out_row_stride +
+                      static_cast<int64_t>(t.g * kG + h) * a.out_head_stride;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint32_t o[32];
+        if (blocks) {
+          tc::ld32(to + 32 * c, o);
+          tc::wait_ld();
+        }
+        if (live) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            uint32_t w[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const float y0 = __uint_as_float(o[8 * q + 2 * j]) * inv * f1 * f2;
+              const float y1 = __uint_as_float(o[8 * q + 2 * j + 1]) * inv * f1 * f2;
+              w[j] = l != 0.f ? pack_bf16(y0, y1) : 0u;  // no key: O was never written, or holds zeros
+            }
+            *reinterpret_cast<uint4*>(dst + 32 * c + 8 * q) = make_uint4(w[0], w[1], w[2], w[3]);
+          }
+        }
+      }
+      if (live && a.lse != nullptr)
+        a.lse[static_cast<int64_t>(t.t0 + x * T + tok) * a.lse_row_stride + t.g * kG + h] =
+            l != 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+      tc::fence_before_sync();
+    }
+  } else {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
   if (warp == 2) {
     // ------------------------------------------------------------------ scheduler
     int total = 0;  // request tiles
@@ -531,174 +718,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
         if (issued[x] > done[x]) mbar_wait_bounded(&ctl->s_full[x], (issued[x] - 1) & 1, kWaitNs);
       }
     }
-  } else if (warp >= 4) {
-    // ------------------------------------------------------------------ softmax and output
-    const int x = (warp - 4) >> 2, quad = warp & 3;
-    const int row = quad * 32 + lane;
-    const int tok = row / kG, h = row % kG;
-    const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
-    const uint32_t ts = tmem + x * 128 + lane_off, to = tmem + 256 + x * 128 + lane_off;
-    const float sl2 = a.scale_log2;
-    int ns = 0;  // blocks of this MMA tile so far
-    bool ok = true;
-    for (int k = 0; ok; ++k) {
-      if (!warp_wait_on(&ctl->tile_full[k & 1], (k >> 1) & 1, ctl, a.err_word)) break;
-      const Tile t = ctl->tile[k & 1];
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&ctl->tile_empty[k & 1]);
-      if (t.end || aborted(ctl)) break;
-      int pa, pb;
-      tile_rows<kG>(t, x, &pa, &pb);
-      const bool live = x * T + tok < t.n_tok;
-      const int p = pa + tok;
-      float m = -INFINITY, l = 0.f;
-      int E = 0;
-      bool started = false;  // the tile has had a block: O holds something
-      for (int i = 0; i < t.count; ++i) {
-        const int b = tile_block(t, i), n0 = b * kSparseBlock;
-        if (!block_seen(a, n0, pa, pb)) continue;
-        const int info = __ldg(a.image_info + static_cast<int64_t>(t.slot0 + (b < t.req_head ? b : t.req_head + b - t.req_first)) *
-                                                  a.num_kv_heads + t.g);
-        const bool whole = (info >> 8) == 0xff && n0 + kSparseBlock - 1 <= pa &&
-                           (a.window == 0 || n0 > pb - a.window || n0 + kSparseBlock <= a.num_sinks);
-        if (!warp_wait_on(&ctl->s_full[x], ns & 1, ctl, a.err_word)) {
-          ok = false;
-          break;
-        }
-        tc::fence_after_sync();
-        uint32_t v[128];
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tc::ld32(ts + 32 * c, *reinterpret_cast<uint32_t(*)[32]>(&v[32 * c]));
-        tc::wait_ld();
-        bool any = live;  // does this row see a key of the block
-        if (!whole) {
-          uint32_t bits[4];
-          any = false;
-#pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            // keys 32c .. 32c + 31 of the block
-            const int base = n0 + 32 * c, behind = p - base;
-            uint32_t w = !live || behind < 0 ? 0u : behind >= 31 ? 0xffffffffu : (2u << behind) - 1u;
-            if (a.window > 0) {
-              const int lo = p - a.window + 1 - base, s = a.num_sinks - base;
-              const uint32_t in = lo <= 0 ? 0xffffffffu : lo > 31 ? 0u : 0xffffffffu << lo;
-              const uint32_t sink = s <= 0 ? 0u : s >= 32 ? 0xffffffffu : (1u << s) - 1u;
-              w &= in | sink;
-            }
-            w &= (((info >> (8 + 2 * c)) & 1) ? 0xffffu : 0u) | (((info >> (9 + 2 * c)) & 1) ? 0xffff0000u : 0u);
-            bits[c] = w;
-            any |= w != 0u;
-          }
-#pragma unroll
-          for (int j = 0; j < 128; ++j)
-            if (!(bits[j >> 5] & (1u << (j & 31)))) v[j] = 0xff800000u;  // -inf
-        }
-        float mx0 = __uint_as_float(v[0]), mx1 = __uint_as_float(v[1]);
-#pragma unroll
-        for (int j = 2; j < 128; j += 2) {
-          mx0 = fmaxf(mx0, __uint_as_float(v[j]));
-          mx1 = fmaxf(mx1, __uint_as_float(v[j + 1]));
-        }
-        const float mxs = fmaxf(mx0, mx1) * sl2;  // sl2 > 0
-        // move the reference and the exponent, rescale O
-        float f = 1.f;
-        if (any && mxs > m + kLazyLog2) {
-          f = ex2(m - mxs);  // 0 on the row's first keys
-          l *= f;
-          m = mxs;
-        }
-        const int e = info & 0xff;
-        int de = 0;
-        if (any && e != 0) {
-          de = e - kInfoBias - E;
-          if (!started || (de > kExpUp || (de < kExpDown && de >= -100))) {
-            if (started) f *= exp2i(-de);
-            E += de;
-            de = 0;
-          }
-          de = max(de, -60);  // V that far below O adds nothing; the row sum still counts its keys
-        }
-        if (__any_sync(0xffffffffu, f != 1.f)) {
-          if (ns > 0 && !warp_wait_on(&ctl->pv_done[x], (ns - 1) & 1, ctl, a.err_word)) {
-            ok = false;
-            break;
-          }
-          tc::fence_after_sync();
-          if (started) {
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              uint32_t o[32];
-              tc::ld32(to + 32 * c, o);
-              tc::wait_ld();
-#pragma unroll
-              for (int j = 0; j < 32; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f);
-              tc::st32(to + 32 * c, o);
-            }
-          }
-        }
-        // P * 2^de, and the row sum
-        const float mu = (m == -INFINITY ? 0.f : m) - static_cast<float>(de);
-        float2 sum0 = make_float2(0.f, 0.f), sum1 = make_float2(0.f, 0.f);
-        const float2 sc = make_float2(sl2, sl2), off = make_float2(-mu, -mu);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          uint32_t pk[16];
-#pragma unroll
-          for (int j = 0; j < 16; ++j) {
-            const int i0 = 32 * c + 2 * j;
-            float2 z = fma2(make_float2(__uint_as_float(v[i0]), __uint_as_float(v[i0 + 1])), sc, off);
-            z.x = ex2(z.x);
-            z.y = ex2(z.y);
-            if (j & 1) sum1 = add2(sum1, z);
-            else sum0 = add2(sum0, z);
-            pk[j] = pack_f16(z.x, z.y);
-          }
-          tc::st16(ts + 16 * c, pk);
-        }
-        l += (sum0.x + sum0.y + sum1.x + sum1.y) * exp2i(-de);
-        started = true;
-        tc::wait_st();
-        tc::fence_before_sync();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&ctl->p_full[x]);
-        ++ns;
-      }
-      if (!ok) break;
-      // ---- output
-      const bool blocks = __any_sync(0xffffffffu, started);
-      if (blocks && !warp_wait_on(&ctl->pv_done[x], (ns - 1) & 1, ctl, a.err_word)) break;
-      tc::fence_after_sync();
-      // O * 2^E * v_scale / l, in two steps so that no factor leaves fp32's range on its own
-      const float inv = l != 0.f ? a.v_scale / l : 0.f;
-      const float f1 = exp2i(E / 2), f2 = exp2i(E - E / 2);
-      uint16_t* dst = a.out + static_cast<int64_t>(t.t0 + x * T + tok) * a.out_row_stride +
-                      static_cast<int64_t>(t.g * kG + h) * a.out_head_stride;
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        uint32_t o[32];
-        if (blocks) {
-          tc::ld32(to + 32 * c, o);
-          tc::wait_ld();
-        }
-        if (live) {
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            uint32_t w[4];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const float y0 = __uint_as_float(o[8 * q + 2 * j]) * inv * f1 * f2;
-              const float y1 = __uint_as_float(o[8 * q + 2 * j + 1]) * inv * f1 * f2;
-              w[j] = l != 0.f ? pack_bf16(y0, y1) : 0u;  // no key: O was never written, or holds zeros
-            }
-            *reinterpret_cast<uint4*>(dst + 32 * c + 8 * q) = make_uint4(w[0], w[1], w[2], w[3]);
-          }
-        }
-      }
-      if (live && a.lse != nullptr)
-        a.lse[static_cast<int64_t>(t.t0 + x * T + tok) * a.lse_row_stride + t.g * kG + h] =
-            l != 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
-      tc::fence_before_sync();
-    }
+  }
   }
   tc::fence_before_sync();
   __syncthreads();
