@@ -25,6 +25,7 @@
 //    enters as P * 2^(e - E), and E moves when e - E leaves [-8, 7].
 // Blocks are masked per row only where a row's border crosses them; a block that no row of A (or B) sees is
 // skipped for it.
+#include "mbar_wait.cuh"
 #include "pbs_device.cuh"
 #include "pbs_internal.h"
 #include "tc_device.cuh"
@@ -281,10 +282,10 @@ struct Ctl {
 
 constexpr size_t kSmemTc = 2 * kQTile + kRing * kImage + sizeof(Ctl);
 static_assert(kSmemTc <= 232448, "shared memory exceeds 227 KiB");
-constexpr uint32_t kTileUsers = 2 + 8;
+constexpr uint32_t kTileUsers = 1 + 1 + 8;  // loads, MMAs, the softmax warps
 
 __device__ __forceinline__ bool wait_on(uint64_t* bar, uint32_t parity, Ctl* ctl, int32_t* err) {
-  if (mbar_wait_bounded(bar, parity, kWaitNs)) return true;
+  if (mbar_wait_quick(bar, parity, kWaitNs)) return true;
   set_err(err, PBS_DEVERR_TIMEOUT);
   atomicExch(&ctl->abort, 1);
   return false;
@@ -302,6 +303,13 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const void* tmap, uint64_
       : "memory");
 }
 
+// One thread of the (converged) warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+  return r != 0;
+}
+
 // The i-th block of a tile's list.
 __device__ __forceinline__ int tile_block(const Tile& t, int i) { return i < t.head ? i : t.first + i - t.head; }
 
@@ -313,9 +321,16 @@ __device__ __forceinline__ void tile_rows(const Tile& t, int x, int* pa, int* pb
   *pb = t.p0 + min(t.n_tok, (x + 1) * T) - 1;
 }
 
-// Does some row at positions pa .. pb see a key of the block at n0?
-__device__ __forceinline__ bool block_seen(const WindowArgs& a, int n0, int pa, int pb) {
-  return pb >= pa && n0 <= pb && (a.window == 0 || n0 + kSparseBlock - 1 > max(pa, 0) - a.window || n0 < a.num_sinks);
+// Entries of a tile's list that MMA tile x works on: all i < t.head, and x .. y (y < 0: it has no rows).
+template <int kG>
+__device__ __forceinline__ int2 seen_range(const WindowArgs& a, const Tile& t, int x) {
+  int pa, pb;
+  tile_rows<kG>(t, x, &pa, &pb);
+  if (pb < pa || pb < 0) return make_int2(0, -1);
+  const int low = a.window > 0 ? max(0, max(pa, 0) - a.window + 1) : 0;
+  // the block of the first key in the window, or t.first when the sinks reach past t.first
+  const int lo = a.window > 0 && a.num_sinks > t.first * kSparseBlock ? t.first : max(t.first, low / kSparseBlock);
+  return make_int2(t.head + lo - t.first, min(t.count - 1, t.head + pb / kSparseBlock - t.first));
 }
 
 __device__ __forceinline__ float2 fma2(float2 x, float2 y, float2 z) {
@@ -407,9 +422,10 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
       float m = -INFINITY, l = 0.f;
       int E = 0;
       bool started = false;  // the tile has had a block: O holds something
-      for (int i = 0; i < t.count; ++i) {
+      const int2 range = seen_range<kG>(a, t, x);
+      for (int i = 0; i < t.count && range.y >= 0; ++i) {
+        if (i >= t.head && (i < range.x || i > range.y)) continue;
         const int b = tile_block(t, i), n0 = b * kSparseBlock;
-        if (!block_seen(a, n0, pa, pb)) continue;
         const int info = __ldg(a.image_info + static_cast<int64_t>(t.slot0 + (b < t.req_head ? b : t.req_head + b - t.req_first)) *
                                                   a.num_kv_heads + t.g);
         const bool whole = (info >> 8) == 0xff && n0 + kSparseBlock - 1 <= pa &&
@@ -645,78 +661,93 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
       }
       // every copy must land before the CTA exits
       for (int i = max(0, n - kRing); i < n; ++i)
-        if (!mbar_wait_bounded(&ctl->full[i % kRing], (i / kRing) & 1, kWaitNs)) set_err(a.err_word, PBS_DEVERR_TIMEOUT);
+        if (!mbar_wait_quick(&ctl->full[i % kRing], (i / kRing) & 1, kWaitNs)) set_err(a.err_word, PBS_DEVERR_TIMEOUT);
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------------ MMAs
-    if (lane == 0) {
+    if (elect_one()) {
       constexpr uint32_t kIdescS = tc::idesc_f16(128, 128, true, false, false);
       constexpr uint32_t kIdescPV = tc::idesc_f16(128, 128, false, false, true);
-      int n = 0;               // ring entries of the tiles before
-      int issued[2] = {0, 0};  // S of A, of B, over the CTA's tiles
-      int done[2] = {0, 0};    // PV
+      const uint64_t q_desc = tc::smem_desc_sw128(smem_u32(q_s), 16, 1024);
+      const uint64_t k_desc = tc::smem_desc_sw128(smem_u32(ring), 16, 1024);
+      const uint64_t v_desc = tc::smem_desc_sw128(smem_u32(ring), kHalf, 1024);
+      int st = 0;             // ring stage and phase of the next entry
+      uint32_t ph = 0;
+      uint32_t done0 = 0, done1 = 0;  // PVs of A and of B, over the CTA's tiles
       bool ok = true;
-      // O_x += P_x V, V in ring stage st
-      auto pv = [&](int x, int st, bool fresh) {
-        if (!wait_on(&ctl->p_full[x], done[x] & 1, ctl, a.err_word)) return false;
-        tc::fence_after_sync();
-        const uint32_t v = smem_u32(ring + st * kImage);
-#pragma unroll
-        for (int ks = 0; ks < 8; ++ks)
-          tc::mma_ts(tmem + 256 + x * 128, tmem + x * 128 + ks * 8, tc::smem_desc_sw128(v + ks * 2048, kHalf, 1024),
-                     kIdescPV, !(fresh && ks == 0));
-        tc::commit(&ctl->pv_done[x]);
-        ++done[x];
-        return true;
-      };
       for (int k = 0; ok; ++k) {
         if (!wait_on(&ctl->tile_full[k & 1], (k >> 1) & 1, ctl, a.err_word)) break;
-        const Tile t = ctl->tile[k & 1];
+        const Tile* t = &ctl->tile[k & 1];
+        const int count = t->count, head = t->head;
+        int2 ra = {0, 0}, rb = {0, 0};
+        const bool end = t->end != 0;
+        if (!end) {
+          ra = seen_range<kG>(a, *t, 0);
+          rb = seen_range<kG>(a, *t, 1);
+        }
         mbar_arrive(&ctl->tile_empty[k & 1]);
-        if (t.end) break;
+        if (end) break;
         if (!wait_on(&ctl->q_full, k & 1, ctl, a.err_word)) break;
-        int pa[2], pb[2];
-        tile_rows<kG>(t, 0, &pa[0], &pb[0]);
-        tile_rows<kG>(t, 1, &pa[1], &pb[1]);
-        bool pending[2] = {false, false}, fresh[2] = {true, true};
-        // step i: PV of block i - 1, S of block i; ring entries n + 2 i: K(i), n + 2 i + 1: V(i)
-        for (int i = 0; ok && i <= t.count; ++i) {
-          const int nk = n + 2 * i, nv = nk - 1;
-          const bool has_s = i < t.count, has_pv = i > 0;
-          if (has_pv && !wait_on(&ctl->full[nv % kRing], (nv / kRing) & 1, ctl, a.err_word)) ok = false;
-          if (ok && has_s && !wait_on(&ctl->full[nk % kRing], (nk / kRing) & 1, ctl, a.err_word)) ok = false;
-          if (!ok) break;
-          tc::fence_after_sync();
-          const int n0 = has_s ? tile_block(t, i) * kSparseBlock : 0;
-          for (int x = 0; ok && x < 2; ++x) {
-            if (pending[x]) {
-              ok = pv(x, nv % kRing, fresh[x]);
-              fresh[x] = false;
-              pending[x] = false;
-            }
-            if (ok && has_s && block_seen(a, n0, pa[x], pb[x])) {
-              const uint32_t q = smem_u32(q_s + x * kQTile), kk = smem_u32(ring + nk % kRing * kImage);
-#pragma unroll
-              for (int ks = 0; ks < 8; ++ks)
-                tc::mma_ss(tmem + x * 128, tc::smem_desc_sw128(q + (ks >> 2) * kHalf + (ks & 3) * 32, 16, 1024),
-                           tc::smem_desc_sw128(kk + (ks >> 2) * kHalf + (ks & 3) * 32, 16, 1024), kIdescS, ks > 0);
-              tc::commit(&ctl->s_full[x]);
-              ++issued[x];
-              pending[x] = true;
+        // step i: PV of block i - 1, S of block i, of A then of B. The ring holds K(0), V(0), K(1), V(1), ..
+        bool pend0 = false, pend1 = false, fresh0 = true, fresh1 = true;
+        for (int i = 0; i <= count; ++i) {
+          const bool has_s = i < count;
+          int vst = 0;
+          if (i > 0) {
+            vst = st;
+            if (!wait_on(&ctl->full[st], ph, ctl, a.err_word)) ok = false;
+            if (++st == kRing) {
+              st = 0;
+              ph ^= 1;
             }
           }
-          if (has_pv) tc::commit(&ctl->empty[nv % kRing]);
-          if (has_s) tc::commit(&ctl->empty[nk % kRing]);
-          if (i == t.count - 1) tc::commit(&ctl->q_empty);  // the tile's last S
+          if (has_s && !wait_on(&ctl->full[st], ph, ctl, a.err_word)) ok = false;
+          if (!ok) break;
+          const uint64_t vd = v_desc + static_cast<uint32_t>(vst * kImage >> 4);
+          const uint64_t kd = k_desc + static_cast<uint32_t>(st * kImage >> 4);
+          auto work = [&](const int x, bool& pend, bool& fresh, uint32_t& done, const int2 r) {
+            if (pend) {  // O += P V
+              if (!wait_on(&ctl->p_full[x], done & 1, ctl, a.err_word)) return false;
+              tc::fence_after_sync();
+#pragma unroll
+              for (int ks = 0; ks < 8; ++ks)
+                tc::mma_ts(tmem + 256 + x * 128, tmem + x * 128 + ks * 8, vd + (ks * 2048 >> 4), kIdescPV, !(fresh && ks == 0));
+              tc::commit(&ctl->pv_done[x]);
+              ++done;
+              fresh = false;
+            }
+            pend = has_s && (i < head || (i >= r.x && i <= r.y)) && r.y >= 0;
+            if (pend) {  // S = Q K^T
+              tc::fence_after_sync();
+#pragma unroll
+              for (int ks = 0; ks < 8; ++ks) {
+                const uint32_t at = ((ks >> 2) * kHalf + (ks & 3) * 32) >> 4;
+                tc::mma_ss(tmem + x * 128, q_desc + (x * kQTile >> 4) + at, kd + at, kIdescS, ks > 0);
+              }
+              tc::commit(&ctl->s_full[x]);
+            }
+            return true;
+          };
+          ok = work(0, pend0, fresh0, done0, ra) && work(1, pend1, fresh1, done1, rb);
+          if (!ok) break;
+          if (i > 0) tc::commit(&ctl->empty[vst]);
+          if (has_s) {
+            tc::commit(&ctl->empty[st]);
+            if (++st == kRing) {
+              st = 0;
+              ph ^= 1;
+            }
+          }
+          if (i == count - 1 || count == 0) tc::commit(&ctl->q_empty);  // the tile's last S
         }
-        n += 2 * t.count;
-        if (t.count == 0) tc::commit(&ctl->q_empty);
+        if (!ok) {  // a wait gave up: the S in flight must complete before TMEM is released
+          if (pend0) mbar_wait_quick(&ctl->s_full[0], done0 & 1, kWaitNs);
+          if (pend1) mbar_wait_quick(&ctl->s_full[1], done1 & 1, kWaitNs);
+        }
       }
       // every MMA must complete before TMEM is released
-      for (int x = 0; x < 2; ++x) {
-        if (done[x] > 0) mbar_wait_bounded(&ctl->pv_done[x], (done[x] - 1) & 1, kWaitNs);
-        if (issued[x] > done[x]) mbar_wait_bounded(&ctl->s_full[x], (issued[x] - 1) & 1, kWaitNs);
-      }
+      if (done0 > 0) mbar_wait_quick(&ctl->pv_done[0], (done0 - 1) & 1, kWaitNs);
+      if (done1 > 0) mbar_wait_quick(&ctl->pv_done[1], (done1 - 1) & 1, kWaitNs);
     }
   }
   }
