@@ -20,7 +20,6 @@
 // pairs of pages in turn (a stage always belongs to one warp), each with its own online softmax
 // (base 2, lazy reference: O is rescaled when the maximum passes it by 2^8); their partials meet in shared
 // memory at the end of a unit. S^T = K Q^T and O^T += V^T P^T with keys as MMA rows (window_page.cuh).
-#include "mbar_wait.cuh"
 #include "pbs_device.cuh"
 #include "pbs_internal.h"
 #include "window_page.cuh"
@@ -289,7 +288,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<FMT>)
           const int page = __shfl_sync(0xffffffffu, ids, j);
           if (lane == 0) {
             const int stage = static_cast<int>(s % NS);
-            if (s >= NS && !mbar_wait_quick(&ctl->empty[stage], ((s / NS) - 1) & 1, kWaitLimitNs)) {
+            if (s >= NS && !mbar_wait_bounded(&ctl->empty[stage], ((s / NS) - 1) & 1, kWaitLimitNs)) {
               set_err(a.err_word, PBS_DEVERR_TIMEOUT);
               atomicExch(&ctl->abort, 1);
             }
@@ -330,7 +329,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<FMT>)
     // every copy issued must land before the shared memory goes away
     if (lane == 0)
       for (int64_t p = s > NS ? s - NS : 0; p < s; ++p)
-        if (!mbar_wait_quick(&ctl->full[p % NS], (p / NS) & 1, kWaitLimitNs)) {
+        if (!mbar_wait_bounded(&ctl->full[p % NS], (p / NS) & 1, kWaitLimitNs)) {
           set_err(a.err_word, PBS_DEVERR_TIMEOUT);
           break;
         }
@@ -392,7 +391,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<FMT>)
         const int e = first + j + i;
         n0[i] = (e < it.head_pages ? e : it.first_page + (e - it.head_pages)) * kPageRows;
         if (*reinterpret_cast<volatile int32_t*>(&ctl->abort) != 0 ||
-            !mbar_wait_quick(&ctl->full[stage + i], parity, kWaitLimitNs)) {
+            !mbar_wait_bounded(&ctl->full[stage + i], parity, kWaitLimitNs)) {
           set_err(a.err_word, PBS_DEVERR_TIMEOUT);
           atomicExch(&ctl->abort, 1);
         } else if (ctl->ok[stage + i] != 0) {

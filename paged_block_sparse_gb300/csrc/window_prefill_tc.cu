@@ -273,7 +273,9 @@ struct Tile {
 struct Ctl {
   uint64_t q_full, q_empty;
   uint64_t full[kRing], empty[kRing];
-  uint64_t s_full[2], p_full[2], pv_done[2];
+  uint64_t s_full[2], p_full[2];
+  uint64_t pv_done[2];    // the tile's last PV
+  uint64_t drained;       // every MMA of the CTA
   uint64_t tile_full[2], tile_empty[2];
   uint32_t tmem;
   int32_t abort;
@@ -282,7 +284,7 @@ struct Ctl {
 
 constexpr size_t kSmemTc = 2 * kQTile + kRing * kImage + sizeof(Ctl);
 static_assert(kSmemTc <= 232448, "shared memory exceeds 227 KiB");
-constexpr uint32_t kTileUsers = 1 + 1 + 8;  // loads, MMAs, the softmax warps
+constexpr uint32_t kTileUsers = 3 + 8;  // loads, MMAs, gate, the softmax warps
 
 __device__ __forceinline__ bool wait_on(uint64_t* bar, uint32_t parity, Ctl* ctl, int32_t* err) {
   if (mbar_wait_quick(bar, parity, kWaitNs)) return true;
@@ -333,6 +335,9 @@ __device__ __forceinline__ int2 seen_range(const WindowArgs& a, const Tile& t, i
   return make_int2(t.head + lo - t.first, min(t.count - 1, t.head + pb / kSparseBlock - t.first));
 }
 
+// The last entry tile x works on (-1: none).
+__device__ __forceinline__ int last_seen(int2 r, int head) { return r.y < 0 ? -1 : r.y >= r.x ? r.y : head - 1; }
+
 __device__ __forceinline__ float2 fma2(float2 x, float2 y, float2 z) {
   float2 r;
   asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
@@ -378,13 +383,14 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
     ctl->abort = 0;
     mbar_init(&ctl->q_full, 1);
     mbar_init(&ctl->q_empty, 1);
+    mbar_init(&ctl->drained, 1);
     for (int i = 0; i < kRing; ++i) {
       mbar_init(&ctl->full[i], 1);
-      mbar_init(&ctl->empty[i], 1);
+      mbar_init(&ctl->empty[i], 2);  // the MMAs and the gate
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(&ctl->s_full[i], 1);
-      mbar_init(&ctl->p_full[i], 4);
+      mbar_init(&ctl->p_full[i], i == 0 ? 5 : 4);  // A's: the softmax warps and the gate
       mbar_init(&ctl->pv_done[i], 1);
       mbar_init(&ctl->tile_full[i], 1);
       mbar_init(&ctl->tile_empty[i], kTileUsers);
@@ -407,7 +413,8 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
     const uint32_t lane_off = static_cast<uint32_t>(quad * 32) << 16;
     const uint32_t ts = tmem + x * 128 + lane_off, to = tmem + 256 + x * 128 + lane_off;
     const float sl2 = a.scale_log2;
-    int ns = 0;  // blocks of this MMA tile so far
+    int ns = 0;     // blocks of this MMA tile over the CTA's tiles
+    int tiles = 0;  // tiles that had any
     bool ok = true;
     for (int k = 0; ok; ++k) {
       if (!warp_wait_on(&ctl->tile_full[k & 1], (k >> 1) & 1, ctl, a.err_word)) break;
@@ -492,11 +499,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
           de = max(de, -60);  // V that far below O adds nothing; the row sum still counts its keys
         }
         if (__any_sync(0xffffffffu, f != 1.f)) {
-          if (ns > 0 && !warp_wait_on(&ctl->pv_done[x], (ns - 1) & 1, ctl, a.err_word)) {
-            ok = false;
-            break;
-          }
-          tc::fence_after_sync();
+          // (S(i) complete: so is the tile's PV(i - 1), issued before it)
           if (started) {
 #pragma unroll 1
             for (int c = 0; c < 128; c += 16) {  // few registers: the scores stay in theirs
@@ -539,7 +542,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
       if (!ok) break;
       // ---- output
       const bool blocks = __any_sync(0xffffffffu, started);
-      if (blocks && !warp_wait_on(&ctl->pv_done[x], (ns - 1) & 1, ctl, a.err_word)) break;
+      if (blocks && !warp_wait_on(&ctl->pv_done[x], tiles++ & 1, ctl, a.err_word)) break;
       tc::fence_after_sync();
       // O * 2^E * v_scale / l, in two steps so that no factor leaves fp32's range on its own
       const float inv = l != 0.f ? a.v_scale / l : 0.f;
@@ -663,6 +666,42 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
       for (int i = max(0, n - kRing); i < n; ++i)
         if (!mbar_wait_quick(&ctl->full[i % kRing], (i / kRing) & 1, kWaitNs)) set_err(a.err_word, PBS_DEVERR_TIMEOUT);
     }
+  } else if (warp == 3) {
+    // ------------------------------------------------------------------ gate
+    // Waits for a step's V(i - 1) and K(i) and adds the last arrival to A's P barrier, so that the MMA thread,
+    // whose every barrier read is on the critical path, reads one barrier for the three.
+    if (lane == 0) {
+      int st = 0;
+      uint32_t ph = 0, n = 0;
+      bool ok = true;
+      for (int k = 0; ok; ++k) {
+        if (!wait_on(&ctl->tile_full[k & 1], (k >> 1) & 1, ctl, a.err_word)) break;
+        const Tile* t = &ctl->tile[k & 1];
+        const bool end = t->end != 0;
+        const int count = t->count, head = t->head;
+        int2 r = {0, -1};
+        if (!end) r = seen_range<kG>(a, *t, 0);
+        mbar_arrive(&ctl->tile_empty[k & 1]);
+        if (end) break;
+        bool pend = false;
+        for (int i = 0; ok && i <= count; ++i) {
+          for (int e = i > 0 ? 0 : 1; e < (i < count ? 2 : 1); ++e) {  // V(i - 1), K(i)
+            if (!wait_on(&ctl->full[st], ph, ctl, a.err_word)) ok = false;
+            mbar_arrive(&ctl->empty[st]);  // (no stage is loaded twice behind the gate's back)
+            if (++st == kRing) {
+              st = 0;
+              ph ^= 1;
+            }
+          }
+          if (ok && pend) {
+            mbar_arrive(&ctl->p_full[0]);
+            // one arrival a phase
+            if (!wait_on(&ctl->p_full[0], n++ & 1, ctl, a.err_word)) ok = false;
+          }
+          pend = i < count && (i < head || (i >= r.x && i <= r.y)) && r.y >= 0;
+        }
+      }
+    }
   } else if (warp == 1) {
     // ------------------------------------------------------------------ MMAs
     if (elect_one()) {
@@ -690,29 +729,31 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
         if (!wait_on(&ctl->q_full, k & 1, ctl, a.err_word)) break;
         // step i: PV of block i - 1, S of block i, of A then of B. The ring holds K(0), V(0), K(1), V(1), ..
         bool pend0 = false, pend1 = false, fresh0 = true, fresh1 = true;
+        const int last0 = last_seen(ra, head), last1 = last_seen(rb, head);
         for (int i = 0; i <= count; ++i) {
           const bool has_s = i < count;
           int vst = 0;
+          // with a PV of A pending, its P barrier stands for the step's loads too (the gate)
           if (i > 0) {
             vst = st;
-            if (!wait_on(&ctl->full[st], ph, ctl, a.err_word)) ok = false;
+            if (!pend0 && !wait_on(&ctl->full[st], ph, ctl, a.err_word)) ok = false;
             if (++st == kRing) {
               st = 0;
               ph ^= 1;
             }
           }
-          if (has_s && !wait_on(&ctl->full[st], ph, ctl, a.err_word)) ok = false;
+          if (has_s && !pend0 && !wait_on(&ctl->full[st], ph, ctl, a.err_word)) ok = false;
           if (!ok) break;
           const uint64_t vd = v_desc + static_cast<uint32_t>(vst * kImage >> 4);
           const uint64_t kd = k_desc + static_cast<uint32_t>(st * kImage >> 4);
-          auto work = [&](const int x, bool& pend, bool& fresh, uint32_t& done, const int2 r) {
+          auto work = [&](const int x, bool& pend, bool& fresh, uint32_t& done, const int2 r, const int last) {
             if (pend) {  // O += P V
               if (!wait_on(&ctl->p_full[x], done & 1, ctl, a.err_word)) return false;
               tc::fence_after_sync();
 #pragma unroll
               for (int ks = 0; ks < 8; ++ks)
                 tc::mma_ts(tmem + 256 + x * 128, tmem + x * 128 + ks * 8, vd + (ks * 2048 >> 4), kIdescPV, !(fresh && ks == 0));
-              tc::commit(&ctl->pv_done[x]);
+              if (i - 1 == last) tc::commit(&ctl->pv_done[x]);
               ++done;
               fresh = false;
             }
@@ -728,7 +769,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
             }
             return true;
           };
-          ok = work(0, pend0, fresh0, done0, ra) && work(1, pend1, fresh1, done1, rb);
+          ok = work(0, pend0, fresh0, done0, ra, last0) && work(1, pend1, fresh1, done1, rb, last1);
           if (!ok) break;
           if (i > 0) tc::commit(&ctl->empty[vst]);
           if (has_s) {
@@ -740,14 +781,10 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
           }
           if (i == count - 1 || count == 0) tc::commit(&ctl->q_empty);  // the tile's last S
         }
-        if (!ok) {  // a wait gave up: the S in flight must complete before TMEM is released
-          if (pend0) mbar_wait_quick(&ctl->s_full[0], done0 & 1, kWaitNs);
-          if (pend1) mbar_wait_quick(&ctl->s_full[1], done1 & 1, kWaitNs);
-        }
       }
       // every MMA must complete before TMEM is released
-      if (done0 > 0) mbar_wait_quick(&ctl->pv_done[0], (done0 - 1) & 1, kWaitNs);
-      if (done1 > 0) mbar_wait_quick(&ctl->pv_done[1], (done1 - 1) & 1, kWaitNs);
+      tc::commit(&ctl->drained);
+      mbar_wait_quick(&ctl->drained, 0, kWaitNs);
     }
   }
   }
