@@ -36,10 +36,10 @@ constexpr int kOPitch = kHeadDim + 4;  // floats: rows 4 banks apart (conflict-f
 // bf16: 64 KiB of stages per CTA, 2 CTAs per SM; NVFP4: 36 KiB and 3 CTAs (its warps are busy with
 // dequantisation).
 template <int FMT>
-constexpr int kStages = FMT == PBS_KV_BF16 ? 8 : 16;
+constexpr int kStages = FMT == PBS_KV_BF16 ? 4 : 8;  // pairs of pages
 template <int FMT>
 constexpr int kCtasPerSm = FMT == PBS_KV_NVFP4 ? 3 : 2;
-static_assert(kStages<PBS_KV_BF16> % (kPair * kWarps) == 0 && kStages<PBS_KV_NVFP4> % (kPair * kWarps) == 0,
+static_assert(kStages<PBS_KV_BF16> % kWarps == 0 && kStages<PBS_KV_NVFP4> % kWarps == 0,
               "each stage must belong to one consumer warp");
 
 template <int NT>
@@ -53,7 +53,7 @@ template <int FMT>
 struct Ctl {
   uint64_t full[kStages<FMT>];
   uint64_t empty[kStages<FMT>];
-  int32_t ok[kStages<FMT>];  // the stage holds a page (0: padding, or a page that is not in the cache)
+  int32_t ok[kStages<FMT>];  // bit i: the stage holds page i of its pair (else padding, or not in the cache)
   int32_t abort;
   int32_t last;
   int32_t item;              // where this CTA's part begins
@@ -62,7 +62,7 @@ struct Ctl {
 };
 
 template <int FMT, int NT>
-constexpr size_t kSmem = 1024 + size_t(kStages<FMT>) * wp::kStageBytes<FMT> + sizeof(Merge<NT>) + sizeof(Ctl<FMT>);
+constexpr size_t kSmem = 1024 + size_t(kStages<FMT>) * kPair * wp::kStageBytes<FMT> + sizeof(Merge<NT>) + sizeof(Ctl<FMT>);
 
 // One group of rows and its page list.
 struct Item {
@@ -179,7 +179,7 @@ template <int FMT, bool PACKED, int NT>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm<FMT>)
     window_attend_kernel(const __grid_constant__ CUtensorMap tmap, const WindowArgs a) {
   constexpr int NS = kStages<FMT>;
-  constexpr int kStage = wp::kStageBytes<FMT>;
+  constexpr int kPage = wp::kStageBytes<FMT>, kStage = kPair * kPage;
   constexpr int kCols = 8 * NT;
   constexpr int kSlot = kCols * (kHeadDim + 2);  // floats of a workspace partial: O, then m, then l
   extern __shared__ uint8_t smem_raw[];
@@ -258,7 +258,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<FMT>)
 
   if (warp == kWarps) {
     // ---------------------------------------------------------------- producer
-    int64_t s = 0;  // pages issued
+    int st = 0, issued = 0;  // the next pair's stage; pairs issued
+    uint32_t ph = 1;         // phase of its empty barrier (the first round finds the stages empty)
     bool go = true;
     while (go && left > 0) {
       const int end = static_cast<int>(min(static_cast<int64_t>(it.pages), off + left));
@@ -284,39 +285,46 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<FMT>)
         const int ids = next;
         if (base + 32 < end) next = page_of(base + 32 + lane);
         const int n = min(32, end - base);
-        for (int j = 0; go && j < n; ++j, ++s) {
-          const int page = __shfl_sync(0xffffffffu, ids, j);
+        for (int j = 0; j < n; j += kPair) {
+          const int p0 = __shfl_sync(0xffffffffu, ids, j), p1 = __shfl_sync(0xffffffffu, ids, j + 1);
           if (lane == 0) {
-            const int stage = static_cast<int>(s % NS);
-            if (s >= NS && !mbar_wait_bounded(&ctl->empty[stage], ((s / NS) - 1) & 1, kWaitLimitNs)) {
+            if (!mbar_wait_bounded(&ctl->empty[st], ph)) {
               set_err(a.err_word, PBS_DEVERR_TIMEOUT);
               atomicExch(&ctl->abort, 1);
             }
             go = *reinterpret_cast<volatile int32_t*>(&ctl->abort) == 0;
             if (go) {
-              uint8_t* dst = stages + stage * kStage;
-              ctl->ok[stage] = page >= 0;
-              if (page < 0) {
-                mbar_arrive(&ctl->full[stage]);
-              } else {
-                mbar_arrive_expect_tx(&ctl->full[stage], kStage);
+              uint8_t* dst = stages + st * kStage;
+              const int have = (p0 >= 0 ? 1 : 0) | (p1 >= 0 ? 2 : 0);
+              ctl->ok[st] = have;
+              mbar_arrive_expect_tx(&ctl->full[st], ((have & 1) + (have >> 1)) * kPage);
+#pragma unroll
+              for (int i = 0; i < kPair; ++i) {
+                const int page = i == 0 ? p0 : p1;
+                uint8_t* to = dst + i * kPage;
+                if (page < 0) continue;
                 if (FMT != PBS_KV_NVFP4 && PACKED) {
-                  tma_load_5d(dst, &tmap, &ctl->full[stage], page * H + g);
+                  tma_load_5d(to, &tmap, &ctl->full[st], page * H + g);
                 } else if (FMT == PBS_KV_BF16) {
 #pragma unroll
-                  for (int q = 0; q < 4; ++q) tma_load_4d(dst + q * 2048, &tmap, &ctl->full[stage], 64 * q, 0, g, page);
+                  for (int q = 0; q < 4; ++q) tma_load_4d(to + q * 2048, &tmap, &ctl->full[st], 64 * q, 0, g, page);
                 } else if (FMT == PBS_KV_FP8_E4M3) {
 #pragma unroll
-                  for (int q = 0; q < 2; ++q) tma_load_4d(dst + q * 2048, &tmap, &ctl->full[stage], 128 * q, 0, g, page);
+                  for (int q = 0; q < 2; ++q) tma_load_4d(to + q * 2048, &tmap, &ctl->full[st], 128 * q, 0, g, page);
                 } else {
-                  bulk_load(dst, a.kv_cache + static_cast<int64_t>(page) * a.page_stride_bytes + static_cast<int64_t>(g) * kStage,
-                            kStage, &ctl->full[stage]);
+                  bulk_load(to, a.kv_cache + static_cast<int64_t>(page) * a.page_stride_bytes + static_cast<int64_t>(g) * kPage,
+                            kPage, &ctl->full[st]);
                 }
               }
             }
           }
           go = __shfl_sync(0xffffffffu, go, 0);
           if (!go) break;
+          ++issued;
+          if (++st == NS) {
+            st = 0;
+            ph ^= 1;
+          }
         }
       }
       left -= end - off;
@@ -328,8 +336,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<FMT>)
     }
     // every copy issued must land before the shared memory goes away
     if (lane == 0)
-      for (int64_t p = s > NS ? s - NS : 0; p < s; ++p)
-        if (!mbar_wait_bounded(&ctl->full[p % NS], (p / NS) & 1, kWaitLimitNs)) {
+      for (int p = max(0, issued - NS); p < issued; ++p)
+        if (!mbar_wait_bounded(&ctl->full[p % NS], (p / NS) & 1)) {
           set_err(a.err_word, PBS_DEVERR_TIMEOUT);
           break;
         }
@@ -340,7 +348,10 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<FMT>)
   const int hh = lane >> 2, c = lane & 3;
   const int G = a.group, gshift = __ffs(G) - 1;  // a power of two
   const float sl2 = a.scale_log2;
-  int64_t s = 0;  // pages of the CTA's sequence before this unit
+  int64_t s = 0;            // pages of the CTA's sequence before this unit
+  int mine = warp;          // this warp's next pair, counted from the unit's first
+  int st = warp;            // its stage and phase
+  uint32_t ph = 0;
   while (left > 0) {
     const int first = off, end = static_cast<int>(min(static_cast<int64_t>(it.pages), off + left));
     const int n = end - first;  // even
@@ -374,38 +385,41 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<FMT>)
       l[t][0] = l[t][1] = 0.f;
     }
 
-    // this warp's pairs of the unit: pair index (s + j) / 2 of the CTA's sequence, taken in turn
-    const int64_t pair0 = s / kPair;
-    for (int64_t pr = pair0 + ((warp - static_cast<int>(pair0 % kWarps)) + kWarps) % kWarps; pr < pair0 + n / kPair;
-         pr += kWarps) {
-      const int j = static_cast<int>(pr - pair0) * kPair;  // page of the unit's part
-      const int stage = static_cast<int>((pr * kPair) % NS);
-      const uint32_t parity = static_cast<uint32_t>((pr * kPair) / NS) & 1u;
-      uint32_t st[kPair];
+    // pages of the cache that every row of the group sees in full: [whole0, whole1) and the sinks' below
+    // whole1 (rows further on see more of the end and less of the window)
+    const int whole1 = (it.p0 + 1) / kPageRows;
+    const int whole0 = a.window > 0 && it.p1 >= a.window ? (it.p1 - a.window) / kPageRows + 1 : 0;
+    const int whole_sinks = a.num_sinks / kPageRows;
+    const int jump = it.first_page - it.head_pages;
+    // this warp's pairs of the unit: the CTA's pairs are dealt in turn, over all its units
+    const int pairs = n / kPair;
+    for (; mine < pairs; mine += kWarps) {
+      const int e0 = first + mine * kPair;
       int n0[kPair];
-      uint32_t whole = 0u;  // bit i: every row of the group sees all of page i
-      uint32_t real = 0u;
+      bool plain = it.p0 >= 0;
 #pragma unroll
       for (int i = 0; i < kPair; ++i) {
-        st[i] = smem_u32(stages + (stage + i) * kStage);
-        const int e = first + j + i;
-        n0[i] = (e < it.head_pages ? e : it.first_page + (e - it.head_pages)) * kPageRows;
-        if (*reinterpret_cast<volatile int32_t*>(&ctl->abort) != 0 ||
-            !mbar_wait_bounded(&ctl->full[stage + i], parity, kWaitLimitNs)) {
-          set_err(a.err_word, PBS_DEVERR_TIMEOUT);
-          atomicExch(&ctl->abort, 1);
-        } else if (ctl->ok[stage + i] != 0) {
-          real |= 1u << i;
-          if (it.p0 >= n0[i] + kPageRows - 1 &&
-              (a.window == 0 || n0[i] > it.p1 - a.window || n0[i] + kPageRows <= a.num_sinks))
-            whole |= 1u << i;
-        }
+        const int pg = e0 + i < it.head_pages ? e0 + i : e0 + i + jump;
+        n0[i] = pg * kPageRows;
+        plain = plain && pg < whole1 && (pg >= whole0 || pg < whole_sinks);
       }
+      uint32_t real = 0u;
+      if (!mbar_try_wait(&ctl->full[st], ph) &&
+          (*reinterpret_cast<volatile int32_t*>(&ctl->abort) != 0 || !mbar_wait_bounded(&ctl->full[st], ph))) {
+        set_err(a.err_word, PBS_DEVERR_TIMEOUT);
+        atomicExch(&ctl->abort, 1);
+      } else {
+        real = ctl->ok[st];
+      }
+      // (a wait that gave up leaves the pair out, for the whole warp)
       real = __shfl_sync(0xffffffffu, real, 0) & __shfl_sync(0xffffffffu, real, 31);
-      whole = __shfl_sync(0xffffffffu, whole, 0) & real;
+      const uint32_t whole = plain ? real : 0u;
+      uint32_t stp[kPair];
+#pragma unroll
+      for (int i = 0; i < kPair; ++i) stp[i] = smem_u32(stages + st * kStage + i * kPage);
 
       float sc[kPair][NT][4];
-      wp::page_scores<FMT, PACKED, kPair, NT>(st, qf, lane, sc);
+      wp::page_scores<FMT, PACKED, kPair, NT>(stp, qf, lane, sc);
       float mx[NT][2];
 #pragma unroll
       for (int t = 0; t < NT; ++t) mx[t][0] = mx[t][1] = -INFINITY;
@@ -476,7 +490,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<FMT>)
 #pragma unroll
       for (int i = 0; i < kPair; ++i) {
         if ((whole >> i) & 1u) {
-          wp::page_pv<FMT, PACKED, NT, false>(st[i], sc[i], lane, o, 1, [](int) { return 0u; }, row_of);
+          wp::page_pv<FMT, PACKED, NT, false>(stp[i], sc[i], lane, o, 1, [](int) { return 0u; }, row_of);
         } else if ((real >> i) & 1u) {
           uint32_t any = 0u, all = 0xffffu;
           for (int r = 0; r < it.rows; ++r) {
@@ -486,16 +500,19 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<FMT>)
           }
           const int p0 = it.p0;
           wp::page_pv<FMT, PACKED, NT, true>(
-              st[i], sc[i], lane, o, any == all ? 1 : it.rows,
+              stp[i], sc[i], lane, o, any == all ? 1 : it.rows,
               [&](int r) { return any == all ? any : seen_bits(a, n0[i], p0 + r); }, row_of);
         }
       }
       __syncwarp();
-      if (lane == 0) {
-#pragma unroll
-        for (int i = 0; i < kPair; ++i) mbar_arrive(&ctl->empty[stage + i]);
+      if (lane == 0) mbar_arrive(&ctl->empty[st]);
+      st += kWarps;
+      if (st >= NS) {
+        st -= NS;
+        ph ^= 1;
       }
     }
+    mine -= pairs;
 
     // ---- the warps' partials meet
 #pragma unroll

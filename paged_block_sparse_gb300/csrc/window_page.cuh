@@ -56,6 +56,21 @@ __device__ __forceinline__ uint32_t word_of(const uint4& v, int i) {
   return i == 0 ? v.x : i == 1 ? v.y : i == 2 ? v.z : v.w;
 }
 
+// Four e4m3 bytes to two f16x2 words, eight e2m1 codes to four (exact). The converts take a byte or a half
+// of their source register for free; shifting it down first would double the work of the pipe that converts
+// (16 lanes a clock).
+__device__ __forceinline__ void e4m3x4(uint32_t x, uint32_t& lo, uint32_t& hi) {
+  asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+      : "=r"(lo), "=r"(hi)
+      : "r"(x));
+}
+__device__ __forceinline__ void e2m1x8(uint32_t x, uint32_t (&w)[4]) {
+  asm("{\n\t.reg .b8 b0, b1, b2, b3;\n\tmov.b32 {b0, b1, b2, b3}, %4;\n\tcvt.rn.f16x2.e2m1x2 %0, b0;\n\t"
+      "cvt.rn.f16x2.e2m1x2 %1, b1;\n\tcvt.rn.f16x2.e2m1x2 %2, b2;\n\tcvt.rn.f16x2.e2m1x2 %3, b3;\n\t}"
+      : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+      : "r"(x));
+}
+
 // First of the two dims (the second is +8 for bf16, +2 otherwise) of Q fragment word w of k-step j:
 // the order in which page_scores feeds K's dims to the MMA.
 template <int FMT>
@@ -95,8 +110,9 @@ __device__ __forceinline__ void page_scores(const uint32_t (&st)[NP], const uint
       for (int i = 0; i < NP; ++i) {
         const uint32_t w0 = lds32(st[i] + line_off<FMT, PACKED>(hh, 0) + ((j ^ hh) << 4) + 4 * c);
         const uint32_t w1 = lds32(st[i] + line_off<FMT, PACKED>(hh + 8, 0) + ((j ^ hh) << 4) + 4 * c);
-        uint32_t af[4] = {e4m3x2_to_f16x2(w0), e4m3x2_to_f16x2(w1), e4m3x2_to_f16x2(w0 >> 16),
-                          e4m3x2_to_f16x2(w1 >> 16)};
+        uint32_t af[4];
+        e4m3x4(w0, af[0], af[2]);
+        e4m3x4(w1, af[1], af[3]);
 #pragma unroll
         for (int t = 0; t < NT; ++t) mma_f16(s[i][t], af, qf[t][j][0], qf[t][j][1]);
       }
@@ -116,16 +132,19 @@ __device__ __forceinline__ void page_scores(const uint32_t (&st)[NP], const uint
       s1hi[i] = prmt(sc1, sc1, 0x3232);
     }
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
+    for (int j = 0; j < 8; j += 2) {
 #pragma unroll
       for (int i = 0; i < NP; ++i) {
-        const uint32_t w0 = word_of(k0[i], j >> 1) >> (16 * (j & 1));
-        const uint32_t w1 = word_of(k1[i], j >> 1) >> (16 * (j & 1));
         const uint32_t sa = j < 4 ? s0lo[i] : s0hi[i], sb = j < 4 ? s1lo[i] : s1hi[i];
-        uint32_t af[4] = {hmul2(e2m1x2_to_f16x2(w0), sa), hmul2(e2m1x2_to_f16x2(w1), sb),
-                          hmul2(e2m1x2_to_f16x2(w0 >> 8), sa), hmul2(e2m1x2_to_f16x2(w1 >> 8), sb)};
+        uint32_t a[4], b[4];
+        e2m1x8(word_of(k0[i], j >> 1), a);
+        e2m1x8(word_of(k1[i], j >> 1), b);
 #pragma unroll
-        for (int t = 0; t < NT; ++t) mma_f16(s[i][t], af, qf[t][j][0], qf[t][j][1]);
+        for (int h = 0; h < 2; ++h) {
+          uint32_t af[4] = {hmul2(a[2 * h], sa), hmul2(b[2 * h], sb), hmul2(a[2 * h + 1], sa), hmul2(b[2 * h + 1], sb)};
+#pragma unroll
+          for (int t = 0; t < NT; ++t) mma_f16(s[i][t], af, qf[t][j + h][0], qf[t][j + h][1]);
+        }
       }
     }
   }
@@ -218,7 +237,9 @@ __device__ __forceinline__ void page_pv(uint32_t st, const float (&p)[NT][4], in
       const uint32_t sel = (i & 1) ? 0x7362u : 0x5140u;
       const uint32_t x = prmt(word_of(va, i >> 1), word_of(vb, i >> 1), sel);
       const uint32_t y = prmt(word_of(vc, i >> 1), word_of(vd, i >> 1), sel);
-      uint32_t vf[4] = {e4m3x2_to_f16x2(x), e4m3x2_to_f16x2(x >> 16), e4m3x2_to_f16x2(y), e4m3x2_to_f16x2(y >> 16)};
+      uint32_t vf[4];
+      e4m3x4(x, vf[0], vf[1]);
+      e4m3x4(y, vf[2], vf[3]);
       product(i, vf);
     }
   } else {
@@ -237,10 +258,14 @@ __device__ __forceinline__ void page_pv(uint32_t st, const float (&p)[NT][4], in
       const uint32_t hi_ab = ((A >> 4) & 0x0F0F0F0Fu) | (B & 0xF0F0F0F0u);
       const uint32_t lo_cd = (C & 0x0F0F0F0Fu) | ((D & 0x0F0F0F0Fu) << 4);
       const uint32_t hi_cd = ((C >> 4) & 0x0F0F0F0Fu) | (D & 0xF0F0F0F0u);
+      uint32_t la[4], ha[4], lc[4], hc[4];
+      e2m1x8(lo_ab, la);
+      e2m1x8(hi_ab, ha);
+      e2m1x8(lo_cd, lc);
+      e2m1x8(hi_cd, hc);
 #pragma unroll
       for (int b = 0; b < 4; ++b) {
-        uint32_t vf[4] = {hmul2(e2m1x2_to_f16x2(lo_ab >> (8 * b)), sab), hmul2(e2m1x2_to_f16x2(hi_ab >> (8 * b)), sab),
-                          hmul2(e2m1x2_to_f16x2(lo_cd >> (8 * b)), scd), hmul2(e2m1x2_to_f16x2(hi_cd >> (8 * b)), scd)};
+        uint32_t vf[4] = {hmul2(la[b], sab), hmul2(ha[b], sab), hmul2(lc[b], scd), hmul2(hc[b], scd)};
         product(4 * wh + b, vf);
       }
     }
