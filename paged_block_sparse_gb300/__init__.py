@@ -606,7 +606,7 @@ def insert_index_cache(index_k, index_cache, index_slot_mapping, err_word=None, 
 
 def _call(device, fn, where, *args):
     """fn(*args) with `device` current (the library launches on the current device)."""
-    if torch.cuda.current_device() == device.index:
+    if torch._C._cuda_getDevice() == device.index:
         st = fn(*args)
     else:
         with torch.cuda.device(device):
@@ -633,7 +633,7 @@ def _err(err_word, device):
 
 
 def _raw_stream(stream, device):
-    return (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+    return torch._C._cuda_getCurrentRawStream(device.index) if stream is None else stream.cuda_stream
 
 
 def _empty(shape, dtype, device, stream):
@@ -671,17 +671,17 @@ def _window_workspace(kind, need, device, stream):
     """The cached workspace of (kind, device, stream), grown on demand. Calls on one stream run in
     order, so they may share it; a call under graph capture gets memory of the graph's own, so that
     graphs captured on one stream may be replayed side by side."""
-    s = torch.cuda.current_stream(device) if stream is None else stream
+    if stream is not None:
+        with torch.cuda.stream(stream):
+            return _window_workspace(kind, need, device, None)
     make = torch.zeros if kind == "decode" else torch.empty
-    with torch.cuda.stream(s):
-        if torch.cuda.is_current_stream_capturing():
-            return make(need, dtype=torch.uint8, device=device)
-        key = (kind, device.index, s.cuda_stream)
-        ws = _window_workspaces.get(key)
-        if ws is None or ws.numel() < need:
-            _window_workspaces.pop(key, None)
-            ws = make(max(need, 1 << 20), dtype=torch.uint8, device=device)
-            _window_workspaces[key] = ws
+    if torch.cuda.is_current_stream_capturing():
+        return make(need, dtype=torch.uint8, device=device)
+    key = (kind, device.index, torch._C._cuda_getCurrentRawStream(device.index))
+    ws = _window_workspaces.get(key)
+    if ws is None or ws.numel() < need:
+        _window_workspaces.pop(key, None)
+        ws = _window_workspaces[key] = make(max(need, 1 << 20), dtype=torch.uint8, device=device)
     return ws
 
 

@@ -986,19 +986,43 @@ static int make_window_args(pbs::WindowArgs* w, const void* q, int64_t q_row_str
   return PBS_OK;
 }
 
-// Pages a CTA of the split decode kernel takes at least: fewer than four per consumer warp cost
+// Pairs of pages a CTA of the split decode kernel takes at least: fewer than two per consumer warp cost
 // more in merging than the extra CTAs save.
-constexpr int32_t kWindowMinPages = 16;
+constexpr int32_t kWindowMinPairs = 8;
+
+// The map of launch_window_attend.
+static int encode_window_map(CUtensorMap* map, const pbs::WindowArgs& w) {
+  std::memset(map, 0, sizeof(*map));
+  auto enc = tensor_map_encoder();
+  if (enc == nullptr) return PBS_ERR_CUDA;
+  const cuuint64_t heads = static_cast<cuuint64_t>(w.num_kv_heads), pages = static_cast<cuuint64_t>(w.num_pages);
+  const cuuint64_t page = static_cast<cuuint64_t>(w.page_stride_bytes);
+  const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+  void* base = const_cast<uint8_t*>(w.kv_cache);
+  CUresult r;
+  if (w.kv_dtype == PBS_KV_NVFP4) {
+    const cuuint64_t dims[4] = {256, 2 * kNvfp4SlotBytes / 256, heads, pages};
+    const cuuint64_t strides[3] = {256, 2 * kNvfp4SlotBytes, page};
+    const cuuint32_t box[4] = {256, 2 * kNvfp4SlotBytes / 256, 1, 2};
+    r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  } else {
+    const cuuint64_t lines = w.kv_dtype == PBS_KV_BF16 ? 4 : 2;  // 128-byte lines of a row (K, then V)
+    const cuuint64_t dims[5] = {128, kPageRows, lines, heads, pages};
+    const cuuint64_t strides[4] = {128 * lines, 128, 128 * lines * kPageRows, page};
+    const cuuint32_t box[5] = {128, kPageRows, static_cast<cuuint32_t>(lines), 1, 2};
+    r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 5, base, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  }
+  return r == CUDA_SUCCESS ? PBS_OK : PBS_ERR_CUDA;
+}
 
 static int launch_window(const pbs::WindowArgs& w, int sms, pbs_stream_t stream) {
   CUtensorMap map;
-  int32_t packed = 0;
-  const int st = encode_attend_map(&map, w.kv_cache, w.kv_dtype, w.num_kv_heads, w.num_pages, w.page_stride_bytes,
-                                   false, &packed);
+  const int st = encode_window_map(&map, w);
   if (st != PBS_OK) return st;
-  return pbs::launch_window_attend(w, map, packed != 0, sms, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
-             ? PBS_OK
-             : PBS_ERR_CUDA;
+  return pbs::launch_window_attend(w, map, sms, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? PBS_OK
+                                                                                                      : PBS_ERR_CUDA;
 }
 
 int pbs_window_decode_attention(const void* q, int64_t q_row_stride, int64_t q_head_stride, const void* kv_cache,
@@ -1030,7 +1054,7 @@ int pbs_window_decode_attention(const void* q, int64_t q_row_stride, int64_t q_h
     if (workspace_bytes < pbs::window_workspace_bytes(sms, units)) return PBS_ERR_SHAPE;
     w.split_ws = static_cast<float*>(workspace);
     w.split_tickets = static_cast<int32_t*>(workspace) + (workspace_bytes / sizeof(int32_t) - static_cast<size_t>(units));
-    w.min_pages = kWindowMinPages;
+    w.min_pairs = kWindowMinPairs;
   }
   return launch_window(w, sms, stream);
 }

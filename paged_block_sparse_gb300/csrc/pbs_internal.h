@@ -274,7 +274,7 @@ struct WindowArgs {
   int32_t groups_per_req;   // decode
   float* split_ws;          // non-null: the page sequence is cut evenly between the CTAs
   int32_t* split_tickets;   // one per (group, kv head), zero between calls
-  int32_t min_pages;        // pages a CTA takes at least
+  int32_t min_pairs;        // pairs of pages a CTA takes at least
   // tcgen05 prefill: the images of the blocks its requests see, [slot][kv head], and their info words
   uint8_t* k_images;
   uint8_t* v_images;
@@ -286,9 +286,9 @@ struct WindowArgs {
 void window_geometry(WindowArgs* a, int max_rows);
 // Workspace of the split: partials from the front, tickets in the last bytes.
 size_t window_workspace_bytes(int sms, int64_t units);
-// `tmap`: as for launch_attend (packed: the 5-D one-box-per-(page, head) map).
-cudaError_t launch_window_attend(const WindowArgs& a, const CUtensorMap& tmap, bool packed, int sms,
-                                 cudaStream_t stream);
+// `tmap`: a box is two consecutive pages of one kv head: bf16 / fp8 5-D {128-byte lines, 16 rows, lines of a
+// row, kv head, page}, 128B swizzle; NVFP4 4-D {256 bytes, 9, kv head, page}.
+cudaError_t launch_window_attend(const WindowArgs& a, const CUtensorMap& tmap, int sms, cudaStream_t stream);
 
 // Window prefill on tcgen05 (window_prefill_tc.cu): block images a call needs at most, its workspace, and
 // the launch of its two kernels. `q_map`: the tile kernel's Q map (box {64, G, 128 / G}); scale_log2 > 0.

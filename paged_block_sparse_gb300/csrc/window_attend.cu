@@ -5,21 +5,24 @@
 //
 // Units. A group is up to 8 NT / G consecutive rows of one request (G query heads per kv head): its
 // rows x heads are the 8 NT columns of the MMAs, so the rows of a request share every K / V read. An
-// item is a group; its page list is [0, head pages) and then the window's pages up to the last
-// row's own, padded to an even count. A unit is (item, kv head).
+// item is a group. Keys are taken in pairs of pages (32 keys, aligned, so a pair never leaves its block):
+// an item's list is the pairs that hold sinks and then those of the window up to the last row's own. A unit
+// is (item, kv head).
 //
 // Work split. Bound by HBM (bf16, fp8) or by the dequantisation's issue slots (NVFP4), and lengths are
-// ragged, so with a workspace the pages of all units form one sequence that is cut into equal parts, one
-// per resident CTA: every CTA streams the same number of pages, whatever the batch. A CTA's part may end
+// ragged, so with a workspace the pairs of all units form one sequence that is cut into equal parts, one
+// per resident CTA: every CTA streams the same number of pairs, whatever the batch. A CTA's part may end
 // one unit, hold whole ones and begin another; a unit cut between CTAs leaves one partial (max, sum, O)
-// per CTA in the workspace, and the CTA that draws the unit's last ticket merges them in page order
+// per CTA in the workspace, and the CTA that draws the unit's last ticket merges them in pair order
 // (the same bits whoever is last) and clears the ticket. Without a workspace a CTA takes one unit.
 //
-// CTA. One producer warp: page-table entries 32 pages at a time, one TMA box (bf16 / fp8) or bulk copy
-// (NVFP4) per page into a ring of kStages; it runs ahead across unit borders. kWarps consumer warps take
-// pairs of pages in turn (a stage always belongs to one warp), each with its own online softmax
+// CTA. One producer warp: page-table entries of 32 pairs at a time, then one tensor copy per pair into a ring
+// of stages; it runs ahead across unit borders. (Issuing is its cost: with two copies and four warp exchanges
+// a pair, some 700 clocks, it held NVFP4 back.) The consumer warps take pairs in turn (a stage always belongs
+// to one warp), each with its own online softmax
 // (base 2, lazy reference: O is rescaled when the maximum passes it by 2^8); their partials meet in shared
 // memory at the end of a unit. S^T = K Q^T and O^T += V^T P^T with keys as MMA rows (window_page.cuh).
+#include "mbar_wait.cuh"
 #include "pbs_device.cuh"
 #include "pbs_internal.h"
 #include "window_page.cuh"
@@ -27,63 +30,70 @@
 namespace pbs {
 namespace {
 
-constexpr int kWarps = 4;              // consumer warps
-constexpr int kThreads = 32 * (kWarps + 1);
-constexpr int kPair = 2;               // pages per consumer iteration
+constexpr int kPair = 2;               // pages per stage and consumer iteration
 constexpr float kLazyLog2 = 8.0f;
 constexpr int kOPitch = kHeadDim + 4;  // floats: rows 4 banks apart (conflict-free partial writes)
-
-// bf16: 64 KiB of stages per CTA, 2 CTAs per SM; NVFP4: 36 KiB and 3 CTAs (its warps are busy with
-// dequantisation).
-template <int FMT>
-constexpr int kStages = FMT == PBS_KV_BF16 ? 4 : 8;  // pairs of pages
-template <int FMT>
-constexpr int kCtasPerSm = FMT == PBS_KV_NVFP4 ? 3 : 2;
-static_assert(kStages<PBS_KV_BF16> % kWarps == 0 && kStages<PBS_KV_NVFP4> % kWarps == 0,
-              "each stage must belong to one consumer warp");
-
-template <int NT>
-struct Merge {
-  float o[kWarps][8 * NT][kOPitch];
-  float m[kWarps][8 * NT];
-  float l[kWarps][8 * NT];
+// CTAs per SM, consumer warps and stages per CTA. bf16 is bound by HBM: 2 x 4 warps keep up, and 128 KiB per
+// SM are in flight. fp8 and NVFP4 are bound by the pipe that converts (and compares, selects and packs) at 16
+// lanes a clock, not by the number of warps: 32 requests of 8k-64k NVFP4 keys took 304 us with 3 CTAs of 4
+// consumers, 297 with 3 of 3, 303 with 4 of 3, 367 with 2 of 7 (two producers per SM issue too slowly); 128 fp8
+// requests of two rows, 443 us with 2 of 4, 447 with 3 of 3, 450 with 2 of 5.
+template <int FMT, int NT>
+struct Cfg {
+  static constexpr int kWarps = 4;
+  static constexpr int kStages = FMT == PBS_KV_BF16 ? 4 : 2 * kWarps;
+  static constexpr int kCtas = FMT == PBS_KV_NVFP4 && NT == 1 ? 3 : 2;
+  static constexpr int kThreads = 32 * (kWarps + 1);
+  static_assert(kStages % kWarps == 0, "each stage must belong to one consumer warp");
 };
 
-template <int FMT>
+// The warps' partials of one column tile.
+template <int W>
+struct Merge {
+  float o[W][8][kOPitch];
+  float m[W][8];
+  float l[W][8];
+};
+
+template <int NS>
 struct Ctl {
-  uint64_t full[kStages<FMT>];
-  uint64_t empty[kStages<FMT>];
-  int32_t ok[kStages<FMT>];  // bit i: the stage holds page i of its pair (else padding, or not in the cache)
+  uint64_t full[NS];
+  uint64_t empty[NS];
+  int32_t ok[NS];  // bit i: the stage holds page i of its pair (else padding, or not in the cache)
   int32_t abort;
   int32_t last;
-  int32_t item;              // where this CTA's part begins
-  int32_t warp_sums[kWarps + 1];
-  int64_t offset, total;
+  int32_t item;    // where this CTA's part begins
+  int64_t offset;
+  int32_t ids[32]; // first physical page of the producer's next pairs
 };
 
 template <int FMT, int NT>
-constexpr size_t kSmem = 1024 + size_t(kStages<FMT>) * kPair * wp::kStageBytes<FMT> + sizeof(Merge<NT>) + sizeof(Ctl<FMT>);
+constexpr size_t kSmem = 1024 + size_t(Cfg<FMT, NT>::kStages) * kPair * wp::kPageBytes<FMT> +
+                         sizeof(Merge<Cfg<FMT, NT>::kWarps>) + sizeof(Ctl<Cfg<FMT, NT>::kStages>);
 
-// One group of rows and its page list.
+// One group of rows and its list of pairs.
 struct Item {
   int req, row0, rows;  // first of its rows in q, how many
   int p0, p1;           // their positions
-  int head_pages;       // pages [0, head_pages), then
-  int first_page;       // pages first_page ..
-  int real;             // pages of the list
-  int pages;            // real, padded to pairs (one pair at least)
+  int head;             // pairs [0, head), then
+  int first;            // pairs first ..
+  int real;             // pairs of the list
+  int pairs;            // as scheduled: one at least
 };
 
-__device__ __forceinline__ void page_list(const WindowArgs& a, Item& it) {
-  it.head_pages = it.first_page = it.real = 0;
+constexpr int kPairKeys = kPair * kPageRows;
+constexpr int kPairsPerBlock = kSparseBlock / kPairKeys;
+
+__device__ __forceinline__ void pair_list(const WindowArgs& a, Item& it) {
+  it.head = it.first = it.real = 0;
   if (it.p1 >= 0) {
     const int low = a.window > 0 ? max(0, max(it.p0, 0) - a.window + 1) : 0;
     const int head = min(a.num_sinks, low);
-    it.first_page = low / kPageRows;
-    it.head_pages = min((head + kPageRows - 1) / kPageRows, it.first_page);
-    it.real = it.head_pages + it.p1 / kPageRows - it.first_page + 1;
+    it.first = low / kPairKeys;
+    it.head = min((head + kPairKeys - 1) / kPairKeys, it.first);
+    it.real = it.head + it.p1 / kPairKeys - it.first + 1;
   }
-  it.pages = max(kPair, (it.real + kPair - 1) / kPair * kPair);
+  it.pairs = max(1, it.real);
 }
 
 __device__ __forceinline__ Item decode_item(const WindowArgs& a, int item) {
@@ -94,7 +104,7 @@ __device__ __forceinline__ Item decode_item(const WindowArgs& a, int item) {
   it.row0 = it.req * a.decode_query_len + r0;
   it.p0 = __ldg(a.seq_lens + it.req) - a.decode_query_len + r0;
   it.p1 = it.p0 + it.rows - 1;
-  page_list(a, it);
+  pair_list(a, it);
   return it;
 }
 
@@ -125,7 +135,7 @@ __device__ __forceinline__ Item prefill_item(const WindowArgs& a, int item, int 
       it.row0 = c_of + first;
       it.p0 = __ldg(a.seq_lens + it.req) - n_of + first;
       it.p1 = it.p0 + it.rows - 1;
-      if (it.rows > 0) page_list(a, it);
+      if (it.rows > 0) pair_list(a, it);
       return it;
     }
     before += __shfl_sync(0xffffffffu, incl, 31);
@@ -148,15 +158,23 @@ __device__ __forceinline__ uint32_t seen_bits(const WindowArgs& a, int n0, int p
   return m;
 }
 
-__device__ __forceinline__ void tma_load_5d(void* dst, const void* tmap, uint64_t* bar, int c4) {
-  asm volatile(
-      "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%3, %3, %3, %3, %4}], [%2];" ::"r"(smem_u32(dst)),
-      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(smem_u32(bar)), "r"(0), "r"(c4)
-      : "memory");
+// One pair: both pages' K and V of kv head g.
+template <int FMT>
+__device__ __forceinline__ void load_pair(void* dst, const void* tmap, uint64_t* bar, int g, int page) {
+  if (FMT == PBS_KV_NVFP4)
+    tma_load_4d(dst, tmap, bar, 0, 0, g, page);
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %3, %3, %4, %5}], [%2];" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(smem_u32(bar)), "r"(0), "r"(g), "r"(page)
+        : "memory");
 }
 
-__device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, %0;" ::"n"(32 * kWarps) : "memory"); }
+template <int W>
+__device__ __forceinline__ void consumers_sync() {
+  asm volatile("bar.sync 1, %0;" ::"n"(32 * W) : "memory");
+}
 
 __device__ __forceinline__ uint16_t bf16_bits(float x) {
   uint16_t r;
@@ -164,8 +182,8 @@ __device__ __forceinline__ uint16_t bf16_bits(float x) {
   return r;
 }
 
-// First page of part c of `parts` equal parts of `total` pages (an even number).
-__device__ __forceinline__ int64_t cut(int64_t total, int64_t c, int64_t parts) { return total / 2 * c / parts * 2; }
+// First pair of part c of `parts` equal parts of `total` pairs.
+__device__ __forceinline__ int64_t cut(int64_t total, int64_t c, int64_t parts) { return total * c / parts; }
 
 // Output and log-sum-exp of one element, from the merged maximum, sum and O.
 __device__ __forceinline__ void store_out(const WindowArgs& a, int row, int head, int d, float M, float L, float O) {
@@ -175,17 +193,17 @@ __device__ __forceinline__ void store_out(const WindowArgs& a, int row, int head
     a.lse[static_cast<int64_t>(row) * a.lse_row_stride + head] = L != 0.f ? (M + log2f(L)) * kLn2 : -INFINITY;
 }
 
-template <int FMT, bool PACKED, int NT>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm<FMT>)
+template <int FMT, int NT>
+__global__ void __launch_bounds__(Cfg<FMT, NT>::kThreads, Cfg<FMT, NT>::kCtas)
     window_attend_kernel(const __grid_constant__ CUtensorMap tmap, const WindowArgs a) {
-  constexpr int NS = kStages<FMT>;
-  constexpr int kPage = wp::kStageBytes<FMT>, kStage = kPair * kPage;
+  constexpr int kWarps = Cfg<FMT, NT>::kWarps, kThreads = Cfg<FMT, NT>::kThreads, NS = Cfg<FMT, NT>::kStages;
+  constexpr int kPage = wp::kPageBytes<FMT>, kStage = kPair * kPage;
   constexpr int kCols = 8 * NT;
   constexpr int kSlot = kCols * (kHeadDim + 2);  // floats of a workspace partial: O, then m, then l
   extern __shared__ uint8_t smem_raw[];
   uint8_t* stages = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  Merge<NT>* mg = reinterpret_cast<Merge<NT>*>(stages + NS * kStage);
-  Ctl<FMT>* ctl = reinterpret_cast<Ctl<FMT>*>(mg + 1);
+  Merge<kWarps>* mg = reinterpret_cast<Merge<kWarps>*>(stages + NS * kStage);
+  Ctl<NS>* ctl = reinterpret_cast<Ctl<NS>*>(mg + 1);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const bool split = a.split_ws != nullptr;
   const int H = a.num_kv_heads;
@@ -199,7 +217,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<FMT>)
     fence_mbar_init();
   }
 
-  // ---- this CTA's part of the page sequence: `left` pages from page `off` of unit (item, g)
+  // ---- this CTA's part of the sequence: `left` pairs from pair `off` of unit (item, g)
   int item, g;
   int off = 0;
   int64_t left, parts = 1, total = 0, start = 0;
@@ -208,9 +226,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<FMT>)
     const int n_items = a.num_reqs * a.groups_per_req;
     const int per = (n_items + kThreads - 1) / kThreads;
     const int i0 = min(static_cast<int>(threadIdx.x) * per, n_items), i1 = min(i0 + per, n_items);
-    // pages per kv head fit 32 bits: an item has at most 2^27, so sums are kept in 64
-    int64_t mine = 0;
-    for (int i = i0; i < i1; ++i) mine += decode_item(a, i).pages;
+    int64_t mine = 0;  // an item has up to 2^26 pairs: sums in 64 bits
+    for (int i = i0; i < i1; ++i) mine += decode_item(a, i).pairs;
     int64_t incl = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -226,14 +243,14 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<FMT>)
       total += sums[w];
     }
     total *= H;
-    parts = min(static_cast<int64_t>(gridDim.x), max(int64_t(1), total / a.min_pages));
+    parts = min(static_cast<int64_t>(gridDim.x), max(int64_t(1), total / a.min_pairs));
     if (blockIdx.x >= parts) return;
     start = cut(total, blockIdx.x, parts);
     left = cut(total, blockIdx.x + 1, parts) - start;
     if (start >= before * H && start < (before + mine) * H) {
       int64_t at = before * H;
       for (int i = i0; i < i1; ++i) {
-        const int64_t w = static_cast<int64_t>(decode_item(a, i).pages) * H;
+        const int64_t w = static_cast<int64_t>(decode_item(a, i).pairs) * H;
         if (start < at + w) {
           ctl->item = i;
           ctl->offset = start - at;
@@ -245,15 +262,15 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<FMT>)
     __syncthreads();
     item = ctl->item;
     it = decode_item(a, item);
-    g = static_cast<int>(ctl->offset / it.pages);
-    off = static_cast<int>(ctl->offset % it.pages);
+    g = static_cast<int>(ctl->offset / it.pairs);
+    off = static_cast<int>(ctl->offset % it.pairs);
   } else {
     __syncthreads();
     item = blockIdx.x;
     g = blockIdx.y;
     it = a.cu_seqlens_q != nullptr ? prefill_item(a, item, lane) : decode_item(a, item);
     if (it.rows <= 0) return;
-    left = it.pages;
+    left = it.pairs;
   }
 
   if (warp == kWarps) {
@@ -262,70 +279,56 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<FMT>)
     uint32_t ph = 1;         // phase of its empty barrier (the first round finds the stages empty)
     bool go = true;
     while (go && left > 0) {
-      const int end = static_cast<int>(min(static_cast<int64_t>(it.pages), off + left));
+      const int end = static_cast<int>(min(static_cast<int64_t>(it.pairs), off + left));
       const int32_t* pt_row = a.page_table + static_cast<int64_t>(it.req) * a.pt_row_stride;
-      auto page_of = [&](int i) -> int {  // physical page of entry i of the unit's list, -1: none
+      auto page_of = [&](int i) -> int {  // first physical page of entry i of the unit's list, -1: none
         if (i >= min(end, it.real)) return -1;
-        const int pg = i < it.head_pages ? i : it.first_page + (i - it.head_pages);
-        const int b = pg / kPagesPerBlock;
+        const int pn = i < it.head ? i : it.first + (i - it.head);
+        const int b = pn / kPairsPerBlock;
         if (b >= a.max_blocks) {
           set_err(a.err_word, PBS_DEVERR_BLOCK_OOB);
           return -1;
         }
         const int phys = __ldg(pt_row + b);
-        const int64_t page = static_cast<int64_t>(phys) * a.block_page_stride + pg % kPagesPerBlock;
-        if (phys < 0 || page >= a.num_pages) {
+        const int64_t page = static_cast<int64_t>(phys) * a.block_page_stride + pn % kPairsPerBlock * kPair;
+        // (the second page may lie behind the last key: then it is not missed)
+        if (phys < 0 || page >= a.num_pages || (page + 1 >= a.num_pages && pn * kPairKeys + kPageRows <= it.p1))
           set_err(a.err_word, PBS_DEVERR_PAGE_OOB);
-          return -1;
-        }
-        return static_cast<int>(page);
+        return phys < 0 || page >= a.num_pages ? -1 : static_cast<int>(page);
       };
       int next = page_of(off + lane);
       for (int base = off; go && base < end; base += 32) {
-        const int ids = next;
+        __syncwarp();
+        ctl->ids[lane] = next;
+        __syncwarp();
         if (base + 32 < end) next = page_of(base + 32 + lane);
-        const int n = min(32, end - base);
-        for (int j = 0; j < n; j += kPair) {
-          const int p0 = __shfl_sync(0xffffffffu, ids, j), p1 = __shfl_sync(0xffffffffu, ids, j + 1);
-          if (lane == 0) {
-            if (!mbar_wait_bounded(&ctl->empty[st], ph)) {
+        if (lane == 0) {
+          const int n = min(32, end - base);
+          for (int j = 0; j < n; ++j) {
+            if (!mbar_wait_quick(&ctl->empty[st], ph, kWaitLimitNs)) {
               set_err(a.err_word, PBS_DEVERR_TIMEOUT);
               atomicExch(&ctl->abort, 1);
             }
-            go = *reinterpret_cast<volatile int32_t*>(&ctl->abort) == 0;
-            if (go) {
-              uint8_t* dst = stages + st * kStage;
-              const int have = (p0 >= 0 ? 1 : 0) | (p1 >= 0 ? 2 : 0);
-              ctl->ok[st] = have;
-              mbar_arrive_expect_tx(&ctl->full[st], ((have & 1) + (have >> 1)) * kPage);
-#pragma unroll
-              for (int i = 0; i < kPair; ++i) {
-                const int page = i == 0 ? p0 : p1;
-                uint8_t* to = dst + i * kPage;
-                if (page < 0) continue;
-                if (FMT != PBS_KV_NVFP4 && PACKED) {
-                  tma_load_5d(to, &tmap, &ctl->full[st], page * H + g);
-                } else if (FMT == PBS_KV_BF16) {
-#pragma unroll
-                  for (int q = 0; q < 4; ++q) tma_load_4d(to + q * 2048, &tmap, &ctl->full[st], 64 * q, 0, g, page);
-                } else if (FMT == PBS_KV_FP8_E4M3) {
-#pragma unroll
-                  for (int q = 0; q < 2; ++q) tma_load_4d(to + q * 2048, &tmap, &ctl->full[st], 128 * q, 0, g, page);
-                } else {
-                  bulk_load(to, a.kv_cache + static_cast<int64_t>(page) * a.page_stride_bytes + static_cast<int64_t>(g) * kPage,
-                            kPage, &ctl->full[st]);
-                }
-              }
+            if (*reinterpret_cast<volatile int32_t*>(&ctl->abort) != 0) {
+              go = false;
+              break;
+            }
+            const int page = ctl->ids[j];
+            ctl->ok[st] = page < 0 ? 0 : page + 1 < a.num_pages ? 3 : 1;
+            if (page < 0) {
+              mbar_arrive(&ctl->full[st]);
+            } else {
+              mbar_arrive_expect_tx(&ctl->full[st], kStage);
+              load_pair<FMT>(stages + st * kStage, &tmap, &ctl->full[st], g, page);
+            }
+            ++issued;
+            if (++st == NS) {
+              st = 0;
+              ph ^= 1;
             }
           }
-          go = __shfl_sync(0xffffffffu, go, 0);
-          if (!go) break;
-          ++issued;
-          if (++st == NS) {
-            st = 0;
-            ph ^= 1;
-          }
         }
+        go = __shfl_sync(0xffffffffu, go, 0);
       }
       left -= end - off;
       off = 0;
@@ -337,7 +340,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<FMT>)
     // every copy issued must land before the shared memory goes away
     if (lane == 0)
       for (int p = max(0, issued - NS); p < issued; ++p)
-        if (!mbar_wait_bounded(&ctl->full[p % NS], (p / NS) & 1)) {
+        if (!mbar_wait_quick(&ctl->full[p % NS], (p / NS) & 1, kWaitLimitNs)) {
           set_err(a.err_word, PBS_DEVERR_TIMEOUT);
           break;
         }
@@ -348,13 +351,13 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<FMT>)
   const int hh = lane >> 2, c = lane & 3;
   const int G = a.group, gshift = __ffs(G) - 1;  // a power of two
   const float sl2 = a.scale_log2;
-  int64_t s = 0;            // pages of the CTA's sequence before this unit
+  int64_t s = 0;            // pairs of the CTA's sequence before this unit
   int mine = warp;          // this warp's next pair, counted from the unit's first
   int st = warp;            // its stage and phase
   uint32_t ph = 0;
   while (left > 0) {
-    const int first = off, end = static_cast<int>(min(static_cast<int64_t>(it.pages), off + left));
-    const int n = end - first;  // even
+    const int first = off, end = static_cast<int>(min(static_cast<int64_t>(it.pairs), off + left));
+    const int n = end - first;
     // Q fragments and each column's row
     uint32_t qf[NT][8][2];
     int row_of[NT][2];
@@ -385,41 +388,32 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<FMT>)
       l[t][0] = l[t][1] = 0.f;
     }
 
-    // pages of the cache that every row of the group sees in full: [whole0, whole1) and the sinks' below
-    // whole1 (rows further on see more of the end and less of the window)
-    const int whole1 = (it.p0 + 1) / kPageRows;
-    const int whole0 = a.window > 0 && it.p1 >= a.window ? (it.p1 - a.window) / kPageRows + 1 : 0;
-    const int whole_sinks = a.num_sinks / kPageRows;
-    const int jump = it.first_page - it.head_pages;
+    // Entries of the list whose 32 keys every row of the group sees: [plain0, plain1) in the window (behind
+    // the first row's position or before the last row's window they are not) and [0, plain_s) of the sinks.
+    const int jump = it.first - it.head;
+    int plain0 = 0, plain1 = 0, plain_s = 0;
+    if (it.p0 >= 0) {
+      const int whole1 = (it.p0 + 1) / kPairKeys;  // pairs before it end at p0 or earlier
+      plain1 = whole1 - jump;
+      plain0 = (a.window > 0 && it.p1 >= a.window ? (it.p1 - a.window) / kPairKeys + 1 : 0) - jump;
+      plain_s = min(min(it.head, whole1), a.num_sinks / kPairKeys);
+    }
     // this warp's pairs of the unit: the CTA's pairs are dealt in turn, over all its units
-    const int pairs = n / kPair;
-    for (; mine < pairs; mine += kWarps) {
-      const int e0 = first + mine * kPair;
-      int n0[kPair];
-      bool plain = it.p0 >= 0;
-#pragma unroll
-      for (int i = 0; i < kPair; ++i) {
-        const int pg = e0 + i < it.head_pages ? e0 + i : e0 + i + jump;
-        n0[i] = pg * kPageRows;
-        plain = plain && pg < whole1 && (pg >= whole0 || pg < whole_sinks);
-      }
-      uint32_t real = 0u;
-      if (!mbar_try_wait(&ctl->full[st], ph) &&
-          (*reinterpret_cast<volatile int32_t*>(&ctl->abort) != 0 || !mbar_wait_bounded(&ctl->full[st], ph))) {
+    for (; mine < n; mine += kWarps) {
+      const int e = first + mine;
+      bool ok = mbar_try_wait(&ctl->full[st], ph);
+      if (!ok && *reinterpret_cast<volatile int32_t*>(&ctl->abort) == 0)
+        ok = mbar_wait_quick(&ctl->full[st], ph, kWaitLimitNs);
+      if (!__all_sync(0xffffffffu, ok)) {  // a wait that gave up leaves the pair out
         set_err(a.err_word, PBS_DEVERR_TIMEOUT);
         atomicExch(&ctl->abort, 1);
-      } else {
-        real = ctl->ok[st];
       }
-      // (a wait that gave up leaves the pair out, for the whole warp)
-      real = __shfl_sync(0xffffffffu, real, 0) & __shfl_sync(0xffffffffu, real, 31);
-      const uint32_t whole = plain ? real : 0u;
-      uint32_t stp[kPair];
-#pragma unroll
-      for (int i = 0; i < kPair; ++i) stp[i] = smem_u32(stages + st * kStage + i * kPage);
+      const uint32_t real = ok ? ctl->ok[st] : 0u;
+      const uint32_t whole = (e >= plain0 && e < plain1) || e < plain_s ? real : 0u;
+      const uint32_t stp[kPair] = {smem_u32(stages) + st * kStage, smem_u32(stages) + st * kStage + kPage};
 
       float sc[kPair][NT][4];
-      wp::page_scores<FMT, PACKED, kPair, NT>(stp, qf, lane, sc);
+      wp::page_scores<FMT, kPair, NT>(stp, qf, lane, sc);
       float mx[NT][2];
 #pragma unroll
       for (int t = 0; t < NT; ++t) mx[t][0] = mx[t][1] = -INFINITY;
@@ -430,11 +424,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<FMT>)
 #pragma unroll
           for (int x = 0; x < 4; ++x) sc[i][t][x] *= sl2;
         if (!((whole >> i) & 1u)) {
+          const int n0 = ((e < it.head ? e : e + jump) * kPair + i) * kPageRows;
 #pragma unroll
           for (int t = 0; t < NT; ++t)
 #pragma unroll
             for (int w = 0; w < 2; ++w) {
-              const uint32_t b = ((real >> i) & 1u) && row_of[t][w] < it.rows ? seen_bits(a, n0[i], it.p0 + row_of[t][w]) : 0u;
+              const uint32_t b = ((real >> i) & 1u) && row_of[t][w] < it.rows ? seen_bits(a, n0, it.p0 + row_of[t][w]) : 0u;
               if (!((b >> hh) & 1u)) sc[i][t][w] = -INFINITY;
               if (!((b >> (hh + 8)) & 1u)) sc[i][t][w + 2] = -INFINITY;
             }
@@ -490,18 +485,19 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<FMT>)
 #pragma unroll
       for (int i = 0; i < kPair; ++i) {
         if ((whole >> i) & 1u) {
-          wp::page_pv<FMT, PACKED, NT, false>(stp[i], sc[i], lane, o, 1, [](int) { return 0u; }, row_of);
+          wp::page_pv<FMT, NT, false>(stp[i], sc[i], lane, o, 1, [](int) { return 0u; }, row_of);
         } else if ((real >> i) & 1u) {
+          const int n0 = ((e < it.head ? e : e + jump) * kPair + i) * kPageRows;
           uint32_t any = 0u, all = 0xffffu;
           for (int r = 0; r < it.rows; ++r) {
-            const uint32_t b = seen_bits(a, n0[i], it.p0 + r);
+            const uint32_t b = seen_bits(a, n0, it.p0 + r);
             any |= b;
             all &= b;
           }
           const int p0 = it.p0;
-          wp::page_pv<FMT, PACKED, NT, true>(
+          wp::page_pv<FMT, NT, true>(
               stp[i], sc[i], lane, o, any == all ? 1 : it.rows,
-              [&](int r) { return any == all ? any : seen_bits(a, n0[i], p0 + r); }, row_of);
+              [&](int r) { return any == all ? any : seen_bits(a, n0, p0 + r); }, row_of);
         }
       }
       __syncwarp();
@@ -512,61 +508,62 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<FMT>)
         ph ^= 1;
       }
     }
-    mine -= pairs;
+    mine -= n;
 
-    // ---- the warps' partials meet
-#pragma unroll
-    for (int d = 4; d < 32; d <<= 1)
-#pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        l[t][0] += __shfl_xor_sync(0xffffffffu, l[t][0], d);
-        l[t][1] += __shfl_xor_sync(0xffffffffu, l[t][1], d);
-      }
+    // ---- the warps' partials meet, one column tile at a time
+    const bool whole_unit = first == 0 && end == it.pairs;
+    const int cols = it.rows * G;
+    const int d = threadIdx.x;  // the first 128 threads: one dim each
+    float* part = nullptr;
+    if (!whole_unit) part = a.split_ws + (2 * static_cast<int64_t>(blockIdx.x) + (first == 0 ? 1 : 0)) * kSlot;
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
 #pragma unroll
+      for (int x = 4; x < 32; x <<= 1) {
+        l[t][0] += __shfl_xor_sync(0xffffffffu, l[t][0], x);
+        l[t][1] += __shfl_xor_sync(0xffffffffu, l[t][1], x);
+      }
+#pragma unroll
       for (int i = 0; i < 8; ++i)
 #pragma unroll
-        for (int x = 0; x < 4; ++x) mg->o[warp][8 * t + 2 * c + (x & 1)][wp::o_dim<FMT>(i, x >> 1, hh)] = o[t][i][x];
+        for (int x = 0; x < 4; ++x) mg->o[warp][2 * c + (x & 1)][wp::o_dim<FMT>(i, x >> 1, hh)] = o[t][i][x];
       if (hh == 0) {
 #pragma unroll
         for (int w = 0; w < 2; ++w) {
-          mg->m[warp][8 * t + 2 * c + w] = m[t][w];
-          mg->l[warp][8 * t + 2 * c + w] = l[t][w];
+          mg->m[warp][2 * c + w] = m[t][w];
+          mg->l[warp][2 * c + w] = l[t][w];
         }
       }
-    }
-    consumers_sync();
-    const bool whole_unit = first == 0 && end == it.pages;
-    const int cols = it.rows * G;
-    const int d = threadIdx.x;  // 128 consumer threads: one dim each
-    float* part = nullptr;
-    if (!whole_unit) part = a.split_ws + (2 * static_cast<int64_t>(blockIdx.x) + (first == 0 ? 1 : 0)) * kSlot;
-    for (int col = 0; col < cols; ++col) {
-      float M = mg->m[0][col];
+      consumers_sync<kWarps>();
+      const int n_cols = min(8, cols - 8 * t);
+      for (int q = 0; q < n_cols && d < kHeadDim; ++q) {
+        float M = mg->m[0][q];
 #pragma unroll
-      for (int w = 1; w < kWarps; ++w) M = fmaxf(M, mg->m[w][col]);
-      float O = 0.f, L = 0.f;
+        for (int w = 1; w < kWarps; ++w) M = fmaxf(M, mg->m[w][q]);
+        float O = 0.f, L = 0.f;
 #pragma unroll
-      for (int w = 0; w < kWarps; ++w) {
-        // without a maximum every weight is 0 (or NaN, which has to stay)
-        const float f = M == -INFINITY ? 1.f : ex2(mg->m[w][col] - M);
-        O += f * mg->o[w][col][d];
-        L += f * mg->l[w][col];
-      }
-      if (whole_unit) {
-        store_out(a, it.row0 + (col >> gshift), g * G + (col & (G - 1)), d, M, L, O);
-      } else {
-        part[col * kHeadDim + d] = O;
-        if (d == 0) {
-          part[kCols * kHeadDim + col] = M;
-          part[kCols * (kHeadDim + 1) + col] = L;
+        for (int w = 0; w < kWarps; ++w) {
+          // without a maximum every weight is 0 (or NaN, which has to stay)
+          const float f = M == -INFINITY ? 1.f : ex2(mg->m[w][q] - M);
+          O += f * mg->o[w][q][d];
+          L += f * mg->l[w][q];
+        }
+        const int col = 8 * t + q;
+        if (whole_unit) {
+          store_out(a, it.row0 + (col >> gshift), g * G + (col & (G - 1)), d, M, L, O);
+        } else {
+          part[col * kHeadDim + d] = O;
+          if (d == 0) {
+            part[kCols * kHeadDim + col] = M;
+            part[kCols * (kHeadDim + 1) + col] = L;
+          }
         }
       }
+      consumers_sync<kWarps>();  // the buffer is free for the next tile or unit
     }
     if (!whole_unit) {
-      // publish, draw a ticket; the unit's last CTA merges its parts in page order
-      const int64_t u0 = start + s - first, u1 = u0 + it.pages;  // the unit's pages in the sequence
+      // publish, draw a ticket; the unit's last CTA merges its parts in pair order
+      const int64_t u0 = start + s - first, u1 = u0 + it.pairs;  // the unit's pairs in the sequence
       int64_t c0 = u0 * parts / total, c1 = (u1 - 1) * parts / total;
       while (c0 > 0 && cut(total, c0, parts) > u0) --c0;
       while (cut(total, c0 + 1, parts) <= u0) ++c0;
@@ -574,12 +571,12 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<FMT>)
       while (c1 + 1 < parts && cut(total, c1 + 1, parts) < u1) ++c1;
       const int64_t unit = static_cast<int64_t>(item) * H + g;
       __threadfence();
-      consumers_sync();
+      consumers_sync<kWarps>();
       if (threadIdx.x == 0) ctl->last = atomicAdd(a.split_tickets + unit, 1) == static_cast<int>(c1 - c0);
-      consumers_sync();
+      consumers_sync<kWarps>();
       if (ctl->last) {
         __threadfence();
-        for (int col = 0; col < cols; ++col) {
+        for (int col = 0; col < cols && d < kHeadDim; ++col) {
           float M = -INFINITY;
           for (int64_t p = c0; p <= c1; ++p)
             M = fmaxf(M, __ldcg(a.split_ws + (2 * p + (p == c0 ? 1 : 0)) * kSlot + kCols * kHeadDim + col));
@@ -595,7 +592,6 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<FMT>)
         if (threadIdx.x == 0) a.split_tickets[unit] = 0;
       }
     }
-    consumers_sync();  // the merge buffer is free for the next unit
     left -= n;
     s += n;
     off = 0;
@@ -606,39 +602,38 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm<FMT>)
   }
 }
 
-template <int FMT, bool PACKED, int NT>
+template <int FMT, int NT>
 cudaError_t launch_one(const WindowArgs& a, const CUtensorMap& tmap, int sms, cudaStream_t stream) {
   constexpr size_t smem = kSmem<FMT, NT>;
-  static_assert(smem * kCtasPerSm<FMT> <= 227 * 1024, "the CTAs of an SM exceed its shared memory");
-  auto kern = window_attend_kernel<FMT, PACKED, NT>;
+  static_assert((smem + 1024) * Cfg<FMT, NT>::kCtas <= 228 * 1024, "the CTAs of an SM exceed its shared memory");
+  auto kern = window_attend_kernel<FMT, NT>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
   if (e != cudaSuccess) return e;
   dim3 grid;
   if (a.split_ws != nullptr) {
-    grid = dim3(static_cast<unsigned>(sms * kCtasPerSm<FMT>));
+    grid = dim3(static_cast<unsigned>(sms * Cfg<FMT, NT>::kCtas));
   } else {
     const int64_t groups = a.cu_seqlens_q != nullptr
                                ? static_cast<int64_t>(a.num_rows) / a.rows_per_group + a.num_reqs
                                : static_cast<int64_t>(a.num_reqs) * a.groups_per_req;
     grid = dim3(static_cast<unsigned>(groups), static_cast<unsigned>(a.num_kv_heads));
   }
-  kern<<<grid, kThreads, smem, stream>>>(tmap, a);
+  kern<<<grid, Cfg<FMT, NT>::kThreads, smem, stream>>>(tmap, a);
   return cudaGetLastError();
 }
 
-template <int FMT, bool PACKED>
+template <int FMT>
 cudaError_t launch_cols(const WindowArgs& a, const CUtensorMap& tmap, int sms, cudaStream_t stream) {
-  return a.rows_per_group * a.group > 8 ? launch_one<FMT, PACKED, 2>(a, tmap, sms, stream)
-                                        : launch_one<FMT, PACKED, 1>(a, tmap, sms, stream);
+  return a.rows_per_group * a.group > 8 ? launch_one<FMT, 2>(a, tmap, sms, stream) : launch_one<FMT, 1>(a, tmap, sms, stream);
 }
 
-constexpr int kMaxCtasPerSm = 3;
+constexpr int kMaxCtas = 4;  // per SM, of any configuration
 constexpr size_t kMaxPartialBytes = 16 * (kHeadDim + 2) * sizeof(float);
 
 }  // namespace
 
 size_t window_workspace_bytes(int sms, int64_t units) {
-  return static_cast<size_t>(sms) * kMaxCtasPerSm * 2 * kMaxPartialBytes + static_cast<size_t>(units) * sizeof(int32_t);
+  return static_cast<size_t>(sms) * kMaxCtas * 2 * kMaxPartialBytes + static_cast<size_t>(units) * sizeof(int32_t);
 }
 
 void window_geometry(WindowArgs* a, int max_rows) {
@@ -648,16 +643,11 @@ void window_geometry(WindowArgs* a, int max_rows) {
   a->groups_per_req = (a->decode_query_len + a->rows_per_group - 1) / a->rows_per_group;
 }
 
-cudaError_t launch_window_attend(const WindowArgs& a, const CUtensorMap& tmap, bool packed, int sms,
-                                 cudaStream_t stream) {
+cudaError_t launch_window_attend(const WindowArgs& a, const CUtensorMap& tmap, int sms, cudaStream_t stream) {
   switch (a.kv_dtype) {
-    case PBS_KV_BF16:
-      return packed ? launch_cols<PBS_KV_BF16, true>(a, tmap, sms, stream)
-                    : launch_cols<PBS_KV_BF16, false>(a, tmap, sms, stream);
-    case PBS_KV_FP8_E4M3:
-      return packed ? launch_cols<PBS_KV_FP8_E4M3, true>(a, tmap, sms, stream)
-                    : launch_cols<PBS_KV_FP8_E4M3, false>(a, tmap, sms, stream);
-    case PBS_KV_NVFP4: return launch_cols<PBS_KV_NVFP4, false>(a, tmap, sms, stream);
+    case PBS_KV_BF16: return launch_cols<PBS_KV_BF16>(a, tmap, sms, stream);
+    case PBS_KV_FP8_E4M3: return launch_cols<PBS_KV_FP8_E4M3>(a, tmap, sms, stream);
+    case PBS_KV_NVFP4: return launch_cols<PBS_KV_NVFP4>(a, tmap, sms, stream);
     default: return cudaErrorInvalidValue;
   }
 }

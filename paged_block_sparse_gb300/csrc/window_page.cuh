@@ -2,9 +2,8 @@
 // S^T = K Q^T and O^T += V^T P^T with the keys as the MMA's M (scores) and K (output) dimension and
 // NT n8-tiles of query columns (a column = one query head of one row of the group).
 //
-// Stage layouts: bf16 [4 quarter rows: K lo, K hi, V lo, V hi][16 rows][128 B] and fp8 [K, V][16
-// rows][128 B], 128B-swizzled (packed caches arrive as one box of 8-row atoms, see line_off); NVFP4
-// the K slot (1152 B) and the V slot as stored.
+// A page in shared memory: bf16 [4 quarter rows: K lo, K hi, V lo, V hi][16 rows][128 B] and fp8 [K, V][16
+// rows][128 B], 128B-swizzled; NVFP4 the K slot (1152 B) and the V slot as stored.
 //
 // A lane (hh = lane / 4, c = lane % 4) holds scores of keys hh, hh + 8 in columns 2c, 2c + 1 of a
 // tile, and V^T fragments of keys 2c, 2c + 1 (first half of the MMA's k) and 2c + 8, 2c + 9.
@@ -16,16 +15,11 @@ namespace pbs {
 namespace wp {
 
 template <int FMT>
-constexpr int kStageBytes = FMT == PBS_KV_BF16 ? 8192 : FMT == PBS_KV_FP8_E4M3 ? 4096 : 2304;
+constexpr int kPageBytes = FMT == PBS_KV_BF16 ? 8192 : FMT == PBS_KV_FP8_E4M3 ? 4096 : 2304;
 constexpr int kNvfp4Slot = 1152;
 
 // Byte offset of the 128-byte line of page row r, quarter q of a bf16 row / half q of an fp8 row.
-template <int FMT, bool PACKED>
-__device__ __forceinline__ uint32_t line_off(int r, int q) {
-  if (!PACKED) return q * 2048 + r * 128;
-  if (FMT == PBS_KV_BF16) return (r >> 3) * 4096 + q * 1024 + (r & 7) * 128;
-  return (r >> 3) * 2048 + q * 1024 + (r & 7) * 128;
-}
+__device__ __forceinline__ uint32_t line_off(int r, int q) { return q * 2048 + r * 128; }
 
 __device__ __forceinline__ uint32_t lds32(uint32_t addr) {
   uint32_t v;
@@ -81,7 +75,7 @@ __device__ __forceinline__ int q_dim(int j, int w, int c) {
 }
 
 // Scores of the pages at st[0..NP): s[page][tile][..]. The pages' chains interleave.
-template <int FMT, bool PACKED, int NP, int NT>
+template <int FMT, int NP, int NT>
 __device__ __forceinline__ void page_scores(const uint32_t (&st)[NP], const uint32_t (&qf)[NT][8][2], int lane,
                                             float (&s)[NP][NT][4]) {
   const int hh = lane >> 2, c = lane & 3;
@@ -98,7 +92,7 @@ __device__ __forceinline__ void page_scores(const uint32_t (&st)[NP], const uint
 #pragma unroll
       for (int i = 0; i < NP; ++i) {
         uint32_t af[4];
-        ldsm_x4(st[i] + line_off<FMT, PACKED>(key, j >> 2) + ((chunk ^ (key & 7)) << 4), af);
+        ldsm_x4(st[i] + line_off(key, j >> 2) + ((chunk ^ (key & 7)) << 4), af);
 #pragma unroll
         for (int t = 0; t < NT; ++t) mma_bf16(s[i][t], af, qf[t][j][0], qf[t][j][1]);
       }
@@ -108,8 +102,8 @@ __device__ __forceinline__ void page_scores(const uint32_t (&st)[NP], const uint
     for (int j = 0; j < 8; ++j) {
 #pragma unroll
       for (int i = 0; i < NP; ++i) {
-        const uint32_t w0 = lds32(st[i] + line_off<FMT, PACKED>(hh, 0) + ((j ^ hh) << 4) + 4 * c);
-        const uint32_t w1 = lds32(st[i] + line_off<FMT, PACKED>(hh + 8, 0) + ((j ^ hh) << 4) + 4 * c);
+        const uint32_t w0 = lds32(st[i] + line_off(hh, 0) + ((j ^ hh) << 4) + 4 * c);
+        const uint32_t w1 = lds32(st[i] + line_off(hh + 8, 0) + ((j ^ hh) << 4) + 4 * c);
         uint32_t af[4];
         e4m3x4(w0, af[0], af[2]);
         e4m3x4(w1, af[1], af[3]);
@@ -165,7 +159,7 @@ __device__ __forceinline__ uint2 key_words(uint32_t bits, int c) {
 // row_bits(r); V of the other keys is cleared in registers before it meets P, since 0 * NaN is NaN.
 // When the rows differ, each row's product goes to a scratch accumulator that is added to that row's
 // columns only.
-template <int FMT, bool PACKED, int NT, bool MASKED, typename RowBits>
+template <int FMT, int NT, bool MASKED, typename RowBits>
 __device__ __forceinline__ void page_pv(uint32_t st, const float (&p)[NT][4], int lane, float (&o)[NT][8][4],
                                         int rows, RowBits row_bits, const int (&row_of)[NT][2]) {
   const int hh = lane >> 2, c = lane & 3;
@@ -224,14 +218,14 @@ __device__ __forceinline__ void page_pv(uint32_t st, const float (&p)[NT][4], in
     for (int i = 0; i < 8; ++i) {
       const int chunk = 2 * (i & 3) + (mi & 1);
       uint32_t vf[4];
-      ldsm_x4_trans(st + line_off<FMT, PACKED>(key, 2 + (i >> 2)) + ((chunk ^ (key & 7)) << 4), vf);
+      ldsm_x4_trans(st + line_off(key, 2 + (i >> 2)) + ((chunk ^ (key & 7)) << 4), vf);
       product(i, vf);
     }
   } else if (FMT == PBS_KV_FP8_E4M3) {
-    const uint4 va = lds128(st + line_off<FMT, PACKED>(2 * c, 1) + ((hh ^ ((2 * c) & 7)) << 4));
-    const uint4 vb = lds128(st + line_off<FMT, PACKED>(2 * c + 1, 1) + ((hh ^ ((2 * c + 1) & 7)) << 4));
-    const uint4 vc = lds128(st + line_off<FMT, PACKED>(2 * c + 8, 1) + ((hh ^ ((2 * c + 8) & 7)) << 4));
-    const uint4 vd = lds128(st + line_off<FMT, PACKED>(2 * c + 9, 1) + ((hh ^ ((2 * c + 9) & 7)) << 4));
+    const uint4 va = lds128(st + line_off(2 * c, 1) + ((hh ^ ((2 * c) & 7)) << 4));
+    const uint4 vb = lds128(st + line_off(2 * c + 1, 1) + ((hh ^ ((2 * c + 1) & 7)) << 4));
+    const uint4 vc = lds128(st + line_off(2 * c + 8, 1) + ((hh ^ ((2 * c + 8) & 7)) << 4));
+    const uint4 vd = lds128(st + line_off(2 * c + 9, 1) + ((hh ^ ((2 * c + 9) & 7)) << 4));
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const uint32_t sel = (i & 1) ? 0x7362u : 0x5140u;
