@@ -980,15 +980,16 @@ static int make_window_args(pbs::WindowArgs* w, const void* q, int64_t q_row_str
   w->out = static_cast<uint16_t*>(out);
   w->out_row_stride = out_row_stride;
   w->out_head_stride = out_head_stride;
+  w->out_vec = aligned(out, 8) && out_row_stride % 4 == 0 && out_head_stride % 4 == 0;
   w->lse = lse;
   w->lse_row_stride = lse_row_stride;
   w->err_word = err_word;
   return PBS_OK;
 }
 
-// Pairs of pages a CTA of the split decode kernel takes at least: fewer than two per consumer warp cost
-// more in merging than the extra CTAs save.
-constexpr int32_t kWindowMinPairs = 8;
+// log2 of the pairs of pages a CTA of the split decode kernel takes at least: fewer than two per consumer
+// warp cost more in merging than the extra CTAs save.
+constexpr int32_t kWindowMinPairsLog2 = 3;
 
 // The map of launch_window_attend.
 static int encode_window_map(CUtensorMap* map, const pbs::WindowArgs& w) {
@@ -1054,7 +1055,7 @@ int pbs_window_decode_attention(const void* q, int64_t q_row_stride, int64_t q_h
     if (workspace_bytes < pbs::window_workspace_bytes(sms, units)) return PBS_ERR_SHAPE;
     w.split_ws = static_cast<float*>(workspace);
     w.split_tickets = static_cast<int32_t*>(workspace) + (workspace_bytes / sizeof(int32_t) - static_cast<size_t>(units));
-    w.min_pairs = kWindowMinPairs;
+    w.min_pairs_log2 = kWindowMinPairsLog2;
   }
   return launch_window(w, sms, stream);
 }

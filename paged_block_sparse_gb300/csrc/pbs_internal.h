@@ -274,7 +274,8 @@ struct WindowArgs {
   int32_t groups_per_req;   // decode
   float* split_ws;          // non-null: the page sequence is cut evenly between the CTAs
   int32_t* split_tickets;   // one per (group, kv head), zero between calls
-  int32_t min_pairs;        // pairs of pages a CTA takes at least
+  int32_t min_pairs_log2;   // log2 of the pairs of pages a CTA takes at least
+  int32_t out_vec;          // out rows and heads start on 8-byte boundaries
   // tcgen05 prefill: the images of the blocks its requests see, [slot][kv head], and their info words
   uint8_t* k_images;
   uint8_t* v_images;

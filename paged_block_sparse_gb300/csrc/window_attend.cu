@@ -176,20 +176,51 @@ __device__ __forceinline__ void consumers_sync() {
   asm volatile("bar.sync 1, %0;" ::"n"(32 * W) : "memory");
 }
 
-__device__ __forceinline__ uint16_t bf16_bits(float x) {
-  uint16_t r;
-  asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(r) : "f"(x));
-  return r;
+__device__ __forceinline__ void add4(float4& o, float f, const float4& x) {
+  o.x += f * x.x;
+  o.y += f * x.y;
+  o.z += f * x.z;
+  o.w += f * x.w;
 }
 
-// First pair of part c of `parts` equal parts of `total` pairs.
-__device__ __forceinline__ int64_t cut(int64_t total, int64_t c, int64_t parts) { return total * c / parts; }
+// The sequence of `total` pairs in `parts` parts: the first `more` have `each` + 1 pairs, the others `each`.
+struct Cut {
+  int64_t each;
+  int more;
+  __device__ __forceinline__ Cut(int64_t total, int parts) {
+    if (total < (int64_t(1) << 31)) {  // 32-bit divisions are the cheap ones
+      each = static_cast<uint32_t>(total) / static_cast<uint32_t>(parts);
+      more = static_cast<int>(static_cast<uint32_t>(total) % static_cast<uint32_t>(parts));
+    } else {
+      each = total / parts;
+      more = static_cast<int>(total % parts);
+    }
+  }
+  __device__ __forceinline__ int64_t first(int c) const { return each * c + min(c, more); }
+  // the part that holds pair x
+  __device__ __forceinline__ int of(int64_t x) const {
+    const int64_t wide = (each + 1) * more, y = x < wide ? x : x - wide, d = x < wide ? each + 1 : each;
+    const int q = y < (int64_t(1) << 31) ? static_cast<int>(static_cast<uint32_t>(y) / static_cast<uint32_t>(d))
+                                          : static_cast<int>(y / d);
+    return x < wide ? q : more + q;
+  }
+};
 
-// Output and log-sum-exp of one element, from the merged maximum, sum and O.
-__device__ __forceinline__ void store_out(const WindowArgs& a, int row, int head, int d, float M, float L, float O) {
-  const float r = L != 0.f ? a.v_scale * O / L : 0.f;  // L is 0 only without keys; NaN goes through
-  a.out[static_cast<int64_t>(row) * a.out_row_stride + static_cast<int64_t>(head) * a.out_head_stride + d] = bf16_bits(r);
-  if (a.lse != nullptr && d == 0)
+// Output dims 4 lane .. and log-sum-exp of one row and head, from the merged maximum, sum and O.
+__device__ __forceinline__ void store_out(const WindowArgs& a, int row, int head, int lane, float M, float L,
+                                          const float4& O) {
+  const float r = L != 0.f ? a.v_scale / L : 0.f;  // L is 0 only without keys (O too); NaN goes through
+  uint16_t* out = a.out + static_cast<int64_t>(row) * a.out_row_stride + static_cast<int64_t>(head) * a.out_head_stride + 4 * lane;
+  const uint32_t lo = pack_bf16(O.x * r, O.y * r), hi = pack_bf16(O.z * r, O.w * r);
+  if (a.out_vec) {
+    *reinterpret_cast<uint2*>(out) = make_uint2(lo, hi);
+  } else {
+    out[0] = static_cast<uint16_t>(lo);
+    out[1] = static_cast<uint16_t>(lo >> 16);
+    out[2] = static_cast<uint16_t>(hi);
+    out[3] = static_cast<uint16_t>(hi >> 16);
+  }
+  if (a.lse != nullptr && lane == 0)
     a.lse[static_cast<int64_t>(row) * a.lse_row_stride + head] = L != 0.f ? (M + log2f(L)) * kLn2 : -INFINITY;
 }
 
@@ -220,13 +251,14 @@ __global__ void __launch_bounds__(Cfg<FMT, NT>::kThreads, Cfg<FMT, NT>::kCtas)
   // ---- this CTA's part of the sequence: `left` pairs from pair `off` of unit (item, g)
   int item, g;
   int off = 0;
-  int64_t left, parts = 1, total = 0, start = 0;
+  int64_t left, start = 0;
+  Cut cut(1, 1);
   Item it;
   if (split) {
     const int n_items = a.num_reqs * a.groups_per_req;
     const int per = (n_items + kThreads - 1) / kThreads;
     const int i0 = min(static_cast<int>(threadIdx.x) * per, n_items), i1 = min(i0 + per, n_items);
-    int64_t mine = 0;  // an item has up to 2^26 pairs: sums in 64 bits
+    int64_t mine = 0, total = 0;  // an item has up to 2^26 pairs: sums in 64 bits
     for (int i = i0; i < i1; ++i) mine += decode_item(a, i).pairs;
     int64_t incl = mine;
 #pragma unroll
@@ -243,10 +275,11 @@ __global__ void __launch_bounds__(Cfg<FMT, NT>::kThreads, Cfg<FMT, NT>::kCtas)
       total += sums[w];
     }
     total *= H;
-    parts = min(static_cast<int64_t>(gridDim.x), max(int64_t(1), total / a.min_pairs));
-    if (blockIdx.x >= parts) return;
-    start = cut(total, blockIdx.x, parts);
-    left = cut(total, blockIdx.x + 1, parts) - start;
+    const int parts = static_cast<int>(min(static_cast<int64_t>(gridDim.x), max(int64_t(1), total >> a.min_pairs_log2)));
+    if (static_cast<int>(blockIdx.x) >= parts) return;
+    cut = Cut(total, parts);
+    start = cut.first(blockIdx.x);
+    left = cut.first(blockIdx.x + 1) - start;
     if (start >= before * H && start < (before + mine) * H) {
       int64_t at = before * H;
       for (int i = i0; i < i1; ++i) {
@@ -262,8 +295,14 @@ __global__ void __launch_bounds__(Cfg<FMT, NT>::kThreads, Cfg<FMT, NT>::kCtas)
     __syncthreads();
     item = ctl->item;
     it = decode_item(a, item);
-    g = static_cast<int>(ctl->offset / it.pairs);
-    off = static_cast<int>(ctl->offset % it.pairs);
+    // the offset lies inside the item: kv heads (at most 65535) x pairs (2^26)
+    const int64_t offset = ctl->offset;
+    if (offset < (int64_t(1) << 31)) {
+      g = static_cast<int>(static_cast<uint32_t>(offset) / static_cast<uint32_t>(it.pairs));
+    } else {
+      g = static_cast<int>(offset / it.pairs);
+    }
+    off = static_cast<int>(offset - static_cast<int64_t>(g) * it.pairs);
   } else {
     __syncthreads();
     item = blockIdx.x;
@@ -485,19 +524,14 @@ __global__ void __launch_bounds__(Cfg<FMT, NT>::kThreads, Cfg<FMT, NT>::kCtas)
 #pragma unroll
       for (int i = 0; i < kPair; ++i) {
         if ((whole >> i) & 1u) {
-          wp::page_pv<FMT, NT, false>(stp[i], sc[i], lane, o, 1, [](int) { return 0u; }, row_of);
+          wp::page_pv<FMT, NT>(stp[i], sc[i], lane, o);
         } else if ((real >> i) & 1u) {
           const int n0 = ((e < it.head ? e : e + jump) * kPair + i) * kPageRows;
-          uint32_t any = 0u, all = 0xffffu;
-          for (int r = 0; r < it.rows; ++r) {
-            const uint32_t b = seen_bits(a, n0, it.p0 + r);
-            any |= b;
-            all &= b;
-          }
+          // what every row sees is what the first row's end and the last row's window leave
           const int p0 = it.p0;
-          wp::page_pv<FMT, NT, true>(
-              stp[i], sc[i], lane, o, any == all ? 1 : it.rows,
-              [&](int r) { return any == all ? any : seen_bits(a, n0, p0 + r); }, row_of);
+          const bool same = it.rows == 1 || (seen_bits(a, n0, p0) == seen_bits(a, n0, it.p1));
+          wp::page_pv_masked<FMT, NT>(stp[i], sc[i], lane, o, same ? 1 : it.rows,
+                                      [&](int r) { return seen_bits(a, n0, p0 + r); }, row_of);
         }
       }
       __syncwarp();
@@ -513,7 +547,6 @@ __global__ void __launch_bounds__(Cfg<FMT, NT>::kThreads, Cfg<FMT, NT>::kCtas)
     // ---- the warps' partials meet, one column tile at a time
     const bool whole_unit = first == 0 && end == it.pairs;
     const int cols = it.rows * G;
-    const int d = threadIdx.x;  // the first 128 threads: one dim each
     float* part = nullptr;
     if (!whole_unit) part = a.split_ws + (2 * static_cast<int64_t>(blockIdx.x) + (first == 0 ? 1 : 0)) * kSlot;
 #pragma unroll
@@ -535,25 +568,27 @@ __global__ void __launch_bounds__(Cfg<FMT, NT>::kThreads, Cfg<FMT, NT>::kCtas)
         }
       }
       consumers_sync<kWarps>();
+      // a warp takes a column, a lane four dims
       const int n_cols = min(8, cols - 8 * t);
-      for (int q = 0; q < n_cols && d < kHeadDim; ++q) {
+      for (int q = warp; q < n_cols; q += kWarps) {
         float M = mg->m[0][q];
 #pragma unroll
         for (int w = 1; w < kWarps; ++w) M = fmaxf(M, mg->m[w][q]);
-        float O = 0.f, L = 0.f;
+        float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+        float L = 0.f;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
           // without a maximum every weight is 0 (or NaN, which has to stay)
           const float f = M == -INFINITY ? 1.f : ex2(mg->m[w][q] - M);
-          O += f * mg->o[w][q][d];
+          add4(O, f, *reinterpret_cast<const float4*>(&mg->o[w][q][4 * lane]));
           L += f * mg->l[w][q];
         }
         const int col = 8 * t + q;
         if (whole_unit) {
-          store_out(a, it.row0 + (col >> gshift), g * G + (col & (G - 1)), d, M, L, O);
+          store_out(a, it.row0 + (col >> gshift), g * G + (col & (G - 1)), lane, M, L, O);
         } else {
-          part[col * kHeadDim + d] = O;
-          if (d == 0) {
+          *reinterpret_cast<float4*>(part + col * kHeadDim + 4 * lane) = O;
+          if (lane == 0) {
             part[kCols * kHeadDim + col] = M;
             part[kCols * (kHeadDim + 1) + col] = L;
           }
@@ -563,31 +598,40 @@ __global__ void __launch_bounds__(Cfg<FMT, NT>::kThreads, Cfg<FMT, NT>::kCtas)
     }
     if (!whole_unit) {
       // publish, draw a ticket; the unit's last CTA merges its parts in pair order
-      const int64_t u0 = start + s - first, u1 = u0 + it.pairs;  // the unit's pairs in the sequence
-      int64_t c0 = u0 * parts / total, c1 = (u1 - 1) * parts / total;
-      while (c0 > 0 && cut(total, c0, parts) > u0) --c0;
-      while (cut(total, c0 + 1, parts) <= u0) ++c0;
-      while (c1 > 0 && cut(total, c1, parts) >= u1) --c1;
-      while (c1 + 1 < parts && cut(total, c1 + 1, parts) < u1) ++c1;
+      const int64_t u0 = start + s - first;  // the unit's first pair in the sequence
+      const int c0 = cut.of(u0), c1 = cut.of(u0 + it.pairs - 1);
       const int64_t unit = static_cast<int64_t>(item) * H + g;
-      __threadfence();
-      consumers_sync<kWarps>();
-      if (threadIdx.x == 0) ctl->last = atomicAdd(a.split_tickets + unit, 1) == static_cast<int>(c1 - c0);
+      if (threadIdx.x == 0) {  // (the warps' stores above came before the barrier: the fence covers them)
+        __threadfence();
+        ctl->last = atomicAdd(a.split_tickets + unit, 1) == c1 - c0;
+        __threadfence();
+      }
       consumers_sync<kWarps>();
       if (ctl->last) {
-        __threadfence();
-        for (int col = 0; col < cols && d < kHeadDim; ++col) {
+        for (int col = warp; col < cols; col += kWarps) {
+          // lane p holds part c0 + p's maximum and sum, 32 parts at a time
+          const auto slot = [&](int c) { return a.split_ws + (2 * static_cast<int64_t>(c) + (c == c0 ? 1 : 0)) * kSlot; };
           float M = -INFINITY;
-          for (int64_t p = c0; p <= c1; ++p)
-            M = fmaxf(M, __ldcg(a.split_ws + (2 * p + (p == c0 ? 1 : 0)) * kSlot + kCols * kHeadDim + col));
-          float O = 0.f, L = 0.f;
-          for (int64_t p = c0; p <= c1; ++p) {
-            const float* from = a.split_ws + (2 * p + (p == c0 ? 1 : 0)) * kSlot;
-            const float f = M == -INFINITY ? 1.f : ex2(__ldcg(from + kCols * kHeadDim + col) - M);
-            O += f * __ldcg(from + col * kHeadDim + d);
-            L += f * __ldcg(from + kCols * (kHeadDim + 1) + col);
+          for (int c = c0 + lane; c <= c1; c += 32) M = fmaxf(M, __ldcg(slot(c) + kCols * kHeadDim + col));
+#pragma unroll
+          for (int x = 16; x > 0; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
+          float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
+          float L = 0.f;
+          for (int base = c0; base <= c1; base += 32) {
+            const int n_parts = min(32, c1 - base + 1);
+            float f = 0.f, l_of = 0.f;
+            if (lane < n_parts) {
+              f = M == -INFINITY ? 1.f : ex2(__ldcg(slot(base + lane) + kCols * kHeadDim + col) - M);
+              l_of = f * __ldcg(slot(base + lane) + kCols * (kHeadDim + 1) + col);
+            }
+#pragma unroll 4
+            for (int p = 0; p < n_parts; ++p) {
+              L += __shfl_sync(0xffffffffu, l_of, p);
+              add4(O, __shfl_sync(0xffffffffu, f, p),
+                   __ldcg(reinterpret_cast<const float4*>(slot(base + p) + col * kHeadDim + 4 * lane)));
+            }
           }
-          store_out(a, it.row0 + (col >> gshift), g * G + (col & (G - 1)), d, M, L, O);
+          store_out(a, it.row0 + (col >> gshift), g * G + (col & (G - 1)), lane, M, L, O);
         }
         if (threadIdx.x == 0) a.split_tickets[unit] = 0;
       }

@@ -152,115 +152,138 @@ __device__ __forceinline__ uint2 key_words(uint32_t bits, int c) {
                     ((b & 1u) ? 0xffffu : 0u) | ((b & 2u) ? 0xffff0000u : 0u));
 }
 
-// O^T += V^T P^T of one page, p[tile][..] laid out as page_scores returns it. bf16 V: P as bf16 hi +
-// lo (two MMAs: P keeps 16 bits); fp8 / NVFP4: V exact in f16, P in f16 (2^-11).
-//
-// MASKED: `bits` are the keys that every row of the group agrees to see (rows == 1), or, per row r,
-// row_bits(r); V of the other keys is cleared in registers before it meets P, since 0 * NaN is NaN.
-// When the rows differ, each row's product goes to a scratch accumulator that is added to that row's
-// columns only.
-template <int FMT, int NT, bool MASKED, typename RowBits>
-__device__ __forceinline__ void page_pv(uint32_t st, const float (&p)[NT][4], int lane, float (&o)[NT][8][4],
-                                        int rows, RowBits row_bits, const int (&row_of)[NT][2]) {
-  const int hh = lane >> 2, c = lane & 3;
-  uint32_t b0[NT], b1[NT], l0[NT], l1[NT];
+// V^T fragment of output-dim tile i (16 dims x 16 keys) of a page.
+template <int FMT>
+struct VPage {
+  uint32_t st;
+  int lane;
+  uint4 a8[FMT == PBS_KV_FP8_E4M3 ? 4 : 1];  // fp8: keys 2c, 2c + 1, 2c + 8, 2c + 9, 16 dims from 16 hh
+  uint32_t w4[4][4];                         // NVFP4: the fragments of 4 tiles ..
+  uint32_t sab, scd;                         // .. before their scales (keys 2c, 2c + 1 | 2c + 8, 2c + 9)
+
+  __device__ __forceinline__ VPage(uint32_t stage, int lane_) : st(stage), lane(lane_) {
+    const int hh = lane >> 2, c = lane & 3;
+    if (FMT == PBS_KV_FP8_E4M3) {
 #pragma unroll
-  for (int t = 0; t < NT; ++t) {
-    if (FMT == PBS_KV_BF16) {
-      const uint32_t h01 = pack_bf16(p[t][0], p[t][1]), h23 = pack_bf16(p[t][2], p[t][3]);
-      b0[t] = movmatrix_trans(h01);
-      b1[t] = movmatrix_trans(h23);
-      l0[t] = movmatrix_trans(pack_bf16(p[t][0] - bf16_lo(h01), p[t][1] - bf16_hi(h01)));
-      l1[t] = movmatrix_trans(pack_bf16(p[t][2] - bf16_lo(h23), p[t][3] - bf16_hi(h23)));
-    } else {
-      b0[t] = movmatrix_trans(pack_f16(p[t][0], p[t][1]));
-      b1[t] = movmatrix_trans(pack_f16(p[t][2], p[t][3]));
+      for (int q = 0; q < 4; ++q) {
+        const int key = 2 * c + (q & 1) + 8 * (q >> 1);
+        a8[q] = lds128(st + line_off(key, 1) + ((hh ^ (key & 7)) << 4));
+      }
+    } else if (FMT == PBS_KV_NVFP4) {
+      const uint32_t vs0 = st + kNvfp4Slot + 1024;
+      sab = e4m3x2_to_f16x2(lds8(vs0 + (2 * c) * 8 + hh) | (lds8(vs0 + (2 * c + 1) * 8 + hh) << 8));
+      scd = e4m3x2_to_f16x2(lds8(vs0 + (2 * c + 8) * 8 + hh) | (lds8(vs0 + (2 * c + 9) * 8 + hh) << 8));
     }
   }
-  auto product = [&](int i, const uint32_t (&vf)[4]) {
-    if (!MASKED) {
-#pragma unroll
-      for (int t = 0; t < NT; ++t) {
-        if (FMT == PBS_KV_BF16) {
-          mma_bf16(o[t][i], vf, b0[t], b1[t]);
-          mma_bf16(o[t][i], vf, l0[t], l1[t]);
-        } else {
-          mma_f16(o[t][i], vf, b0[t], b1[t]);
-        }
-      }
-      return;
+
+  // Tiles 4 half .. 4 half + 3 (NVFP4: unpacks their 8-dim words; elsewhere nothing to do).
+  __device__ __forceinline__ void begin(int half) {
+    if (FMT != PBS_KV_NVFP4) return;
+    const int hh = lane >> 2, c = lane & 3;
+    const uint32_t vc0 = st + kNvfp4Slot + 8 * hh + 4 * half;
+    const uint32_t A = lds32(vc0 + (2 * c) * 64), B = lds32(vc0 + (2 * c + 1) * 64);
+    const uint32_t C = lds32(vc0 + (2 * c + 8) * 64), D = lds32(vc0 + (2 * c + 9) * 64);
+    // a byte of the interleaved words holds one dim of two keys: what one f16x2 word of the fragment wants
+    e2m1x8((A & 0x0F0F0F0Fu) | ((B & 0x0F0F0F0Fu) << 4), w4[0]);
+    e2m1x8(((A >> 4) & 0x0F0F0F0Fu) | (B & 0xF0F0F0F0u), w4[1]);
+    e2m1x8((C & 0x0F0F0F0Fu) | ((D & 0x0F0F0F0Fu) << 4), w4[2]);
+    e2m1x8(((C >> 4) & 0x0F0F0F0Fu) | (D & 0xF0F0F0F0u), w4[3]);
+  }
+
+  __device__ __forceinline__ void tile(int i, uint32_t (&vf)[4]) const {
+    if (FMT == PBS_KV_BF16) {
+      const int mi = lane >> 3;
+      const int key = (lane & 7) + 8 * (mi >> 1), chunk = 2 * (i & 3) + (mi & 1);
+      ldsm_x4_trans(st + line_off(key, 2 + (i >> 2)) + ((chunk ^ (key & 7)) << 4), vf);
+    } else if (FMT == PBS_KV_FP8_E4M3) {
+      const uint32_t sel = (i & 1) ? 0x7362u : 0x5140u;
+      e4m3x4(prmt(word_of(a8[0], i >> 1), word_of(a8[1], i >> 1), sel), vf[0], vf[1]);
+      e4m3x4(prmt(word_of(a8[2], i >> 1), word_of(a8[3], i >> 1), sel), vf[2], vf[3]);
+    } else {
+      const int b = i & 3;
+      vf[0] = hmul2(w4[0][b], sab);
+      vf[1] = hmul2(w4[1][b], sab);
+      vf[2] = hmul2(w4[2][b], scd);
+      vf[3] = hmul2(w4[3][b], scd);
     }
+  }
+};
+
+// P^T as the MMA's B operand. bf16 V: P as bf16 hi + lo (two MMAs: P keeps 16 bits); fp8 / NVFP4: V exact in
+// f16, P in f16 (2^-11).
+template <int FMT, int NT>
+struct PFrag {
+  uint32_t b0[NT], b1[NT], l0[NT], l1[NT];
+  __device__ __forceinline__ explicit PFrag(const float (&p)[NT][4]) {
+#pragma unroll
+    for (int t = 0; t < NT; ++t) {
+      if (FMT == PBS_KV_BF16) {
+        const uint32_t h01 = pack_bf16(p[t][0], p[t][1]), h23 = pack_bf16(p[t][2], p[t][3]);
+        b0[t] = movmatrix_trans(h01);
+        b1[t] = movmatrix_trans(h23);
+        l0[t] = movmatrix_trans(pack_bf16(p[t][0] - bf16_lo(h01), p[t][1] - bf16_hi(h01)));
+        l1[t] = movmatrix_trans(pack_bf16(p[t][2] - bf16_lo(h23), p[t][3] - bf16_hi(h23)));
+      } else {
+        b0[t] = movmatrix_trans(pack_f16(p[t][0], p[t][1]));
+        b1[t] = movmatrix_trans(pack_f16(p[t][2], p[t][3]));
+      }
+    }
+  }
+  __device__ __forceinline__ void mma(int t, float (&o)[4], const uint32_t (&vf)[4]) const {
+    if (FMT == PBS_KV_BF16) {
+      mma_bf16(o, vf, b0[t], b1[t]);
+      mma_bf16(o, vf, l0[t], l1[t]);
+    } else {
+      mma_f16(o, vf, b0[t], b1[t]);
+    }
+  }
+};
+
+// O^T += V^T P^T of one page, p[tile][..] laid out as page_scores returns it.
+template <int FMT, int NT>
+__device__ __forceinline__ void page_pv(uint32_t st, const float (&p)[NT][4], int lane, float (&o)[NT][8][4]) {
+  const PFrag<FMT, NT> pf(p);
+  VPage<FMT> v(st, lane);
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    if ((i & 3) == 0) v.begin(i >> 2);
+    uint32_t vf[4];
+    v.tile(i, vf);
+#pragma unroll
+    for (int t = 0; t < NT; ++t) pf.mma(t, o[t][i], vf);
+  }
+}
+
+// The same for a page that the group's rows see in part. V of the keys that a row does not see is cleared in
+// registers before it meets P, since 0 * NaN is NaN: for all rows alike when they see the same keys
+// (rows == 1), else row by row, each row's product added to its own columns only. bits(r): the keys row r
+// sees; row_of: the lane's columns' rows.
+template <int FMT, int NT, typename Bits>
+__device__ __forceinline__ void page_pv_masked(uint32_t st, const float (&p)[NT][4], int lane, float (&o)[NT][8][4],
+                                               int rows, Bits bits, const int (&row_of)[NT][2]) {
+  const PFrag<FMT, NT> pf(p);
+  VPage<FMT> v(st, lane);
 #pragma unroll 1
-    for (int r = 0; r < rows; ++r) {
-      const uint2 m = key_words(row_bits(r), c);
-      const uint32_t vm[4] = {vf[0] & m.x, vf[1] & m.x, vf[2] & m.y, vf[3] & m.y};
+  for (int r = 0; r < rows; ++r) {
+    const uint2 m = key_words(bits(r), lane & 3);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if ((i & 3) == 0) v.begin(i >> 2);
+      uint32_t vf[4];
+      v.tile(i, vf);
+      vf[0] &= m.x;
+      vf[1] &= m.x;
+      vf[2] &= m.y;
+      vf[3] &= m.y;
 #pragma unroll
       for (int t = 0; t < NT; ++t) {
         float x[4] = {0.f, 0.f, 0.f, 0.f};
-        if (FMT == PBS_KV_BF16) {
-          mma_bf16(x, vm, b0[t], b1[t]);
-          mma_bf16(x, vm, l0[t], l1[t]);
-        } else {
-          mma_f16(x, vm, b0[t], b1[t]);
-        }
+        pf.mma(t, x, vf);
         const bool y0 = rows == 1 || row_of[t][0] == r, y1 = rows == 1 || row_of[t][1] == r;
         o[t][i][0] = y0 ? o[t][i][0] + x[0] : o[t][i][0];
         o[t][i][1] = y1 ? o[t][i][1] + x[1] : o[t][i][1];
         o[t][i][2] = y0 ? o[t][i][2] + x[2] : o[t][i][2];
         o[t][i][3] = y1 ? o[t][i][3] + x[3] : o[t][i][3];
-      }
-    }
-  };
-  if (FMT == PBS_KV_BF16) {
-    const int mi = lane >> 3;
-    const int key = (lane & 7) + 8 * (mi >> 1);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const int chunk = 2 * (i & 3) + (mi & 1);
-      uint32_t vf[4];
-      ldsm_x4_trans(st + line_off(key, 2 + (i >> 2)) + ((chunk ^ (key & 7)) << 4), vf);
-      product(i, vf);
-    }
-  } else if (FMT == PBS_KV_FP8_E4M3) {
-    const uint4 va = lds128(st + line_off(2 * c, 1) + ((hh ^ ((2 * c) & 7)) << 4));
-    const uint4 vb = lds128(st + line_off(2 * c + 1, 1) + ((hh ^ ((2 * c + 1) & 7)) << 4));
-    const uint4 vc = lds128(st + line_off(2 * c + 8, 1) + ((hh ^ ((2 * c + 8) & 7)) << 4));
-    const uint4 vd = lds128(st + line_off(2 * c + 9, 1) + ((hh ^ ((2 * c + 9) & 7)) << 4));
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const uint32_t sel = (i & 1) ? 0x7362u : 0x5140u;
-      const uint32_t x = prmt(word_of(va, i >> 1), word_of(vb, i >> 1), sel);
-      const uint32_t y = prmt(word_of(vc, i >> 1), word_of(vd, i >> 1), sel);
-      uint32_t vf[4];
-      e4m3x4(x, vf[0], vf[1]);
-      e4m3x4(y, vf[2], vf[3]);
-      product(i, vf);
-    }
-  } else {
-    const uint32_t vc0 = st + kNvfp4Slot, vs0 = st + kNvfp4Slot + 1024;
-    const uint2 wa = lds64(vc0 + (2 * c) * 64 + 8 * hh);
-    const uint2 wb = lds64(vc0 + (2 * c + 1) * 64 + 8 * hh);
-    const uint2 wc = lds64(vc0 + (2 * c + 8) * 64 + 8 * hh);
-    const uint2 wd = lds64(vc0 + (2 * c + 9) * 64 + 8 * hh);
-    const uint32_t sab = e4m3x2_to_f16x2(lds8(vs0 + (2 * c) * 8 + hh) | (lds8(vs0 + (2 * c + 1) * 8 + hh) << 8));
-    const uint32_t scd = e4m3x2_to_f16x2(lds8(vs0 + (2 * c + 8) * 8 + hh) | (lds8(vs0 + (2 * c + 9) * 8 + hh) << 8));
-#pragma unroll
-    for (int wh = 0; wh < 2; ++wh) {
-      const uint32_t A = wh ? wa.y : wa.x, B = wh ? wb.y : wb.x;
-      const uint32_t C = wh ? wc.y : wc.x, D = wh ? wd.y : wd.x;
-      const uint32_t lo_ab = (A & 0x0F0F0F0Fu) | ((B & 0x0F0F0F0Fu) << 4);
-      const uint32_t hi_ab = ((A >> 4) & 0x0F0F0F0Fu) | (B & 0xF0F0F0F0u);
-      const uint32_t lo_cd = (C & 0x0F0F0F0Fu) | ((D & 0x0F0F0F0Fu) << 4);
-      const uint32_t hi_cd = ((C >> 4) & 0x0F0F0F0Fu) | (D & 0xF0F0F0F0u);
-      uint32_t la[4], ha[4], lc[4], hc[4];
-      e2m1x8(lo_ab, la);
-      e2m1x8(hi_ab, ha);
-      e2m1x8(lo_cd, lc);
-      e2m1x8(hi_cd, hc);
-#pragma unroll
-      for (int b = 0; b < 4; ++b) {
-        uint32_t vf[4] = {hmul2(la[b], sab), hmul2(ha[b], sab), hmul2(lc[b], scd), hmul2(hc[b], scd)};
-        product(4 * wh + b, vf);
       }
     }
   }
