@@ -33,14 +33,14 @@ namespace {
 constexpr int kPair = 2;               // pages per stage and consumer iteration
 constexpr float kLazyLog2 = 8.0f;
 constexpr int kOPitch = kHeadDim + 4;  // floats: rows 4 banks apart (conflict-free partial writes)
-// CTAs per SM, consumer warps and stages per CTA. bf16 is bound by HBM: 2 x 4 warps keep up, and 128 KiB per
-// SM are in flight. fp8 and NVFP4 are bound by the pipe that converts (and compares, selects and packs) at 16
-// lanes a clock, not by the number of warps: 32 requests of 8k-64k NVFP4 keys took 304 us with 3 CTAs of 4
-// consumers, 297 with 3 of 3, 303 with 4 of 3, 367 with 2 of 7 (two producers per SM issue too slowly); 128 fp8
-// requests of two rows, 443 us with 2 of 4, 447 with 3 of 3, 450 with 2 of 5.
+// CTAs per SM, consumer warps and stages per CTA. bf16 and fp8 are bound by HBM: 2 x 4 (fp8, with converts to do:
+// 2 x 5) warps keep up, 128 to 160 KiB per SM in flight. NVFP4 is bound by the pipe that converts (and compares,
+// selects and packs) at 16 lanes a clock, not by the number of warps: 32 requests of 8k-64k keys took 304 us with
+// 3 CTAs of 4 consumers, 297 with 3 of 3, 303 with 4 of 3, 367 with 2 of 7 (two producers per SM issue too
+// slowly). Two fp8 rows of 128 requests: 344 us with 2 of 5, 356 with 2 of 4, 464 with 3 of 4 and half the stages.
 template <int FMT, int NT>
 struct Cfg {
-  static constexpr int kWarps = 4;
+  static constexpr int kWarps = FMT == PBS_KV_FP8_E4M3 ? 5 : 4;
   static constexpr int kStages = FMT == PBS_KV_BF16 ? 4 : 2 * kWarps;
   static constexpr int kCtas = FMT == PBS_KV_NVFP4 && NT == 1 ? 3 : 2;
   static constexpr int kThreads = 32 * (kWarps + 1);
@@ -65,6 +65,7 @@ struct Ctl {
   int32_t item;    // where this CTA's part begins
   int64_t offset;
   int32_t ids[32]; // first physical page of the producer's next pairs
+  uint2 q[16][32]; // two column tiles: the unit's Q fragments, [tile * 8 + k-step][lane]
 };
 
 template <int FMT, int NT>
@@ -80,6 +81,11 @@ struct Item {
   int real;             // pairs of the list
   int pairs;            // as scheduled: one at least
 };
+
+// What a unit costs beside its pairs (Q, the pairs its borders cross, the merge), in pairs: the sequence that is
+// dealt out holds so many empty places behind each unit's pairs. 44 requests of up to 1.6k keys (three rows, 16
+// heads per kv head): 201 us without them, as the short requests' CTAs end last.
+constexpr int kUnitCost = 12;
 
 constexpr int kPairKeys = kPair * kPageRows;
 constexpr int kPairsPerBlock = kSparseBlock / kPairKeys;
@@ -143,13 +149,13 @@ __device__ __forceinline__ Item prefill_item(const WindowArgs& a, int item, int 
   return it;
 }
 
-// Keys n0 .. n0 + 15 that a row at position p sees, bit n - n0.
-__device__ __forceinline__ uint32_t seen_bits(const WindowArgs& a, int n0, int p) {
-  const int behind = p - n0;  // causal: bits 0 .. behind
+// Keys n0 .. n0 + 15 that rows at positions p_low .. p_high see between them, bit n - n0.
+__device__ __forceinline__ uint32_t seen_bits(const WindowArgs& a, int n0, int p_high, int p_low) {
+  const int behind = p_high - n0;  // causal: bits 0 .. behind
   if (behind < 0) return 0u;
   uint32_t m = behind >= 15 ? 0xffffu : (2u << behind) - 1u;
   if (a.window > 0) {
-    const int lo = p - a.window + 1 - n0;
+    const int lo = max(p_low, 0) - a.window + 1 - n0;
     const uint32_t in = lo <= 0 ? 0xffffu : lo > 15 ? 0u : (0xffffu << lo) & 0xffffu;
     const int s = a.num_sinks - n0;
     const uint32_t sink = s <= 0 ? 0u : s >= 16 ? 0xffffu : (1u << s) - 1u;
@@ -248,7 +254,7 @@ __global__ void __launch_bounds__(Cfg<FMT, NT>::kThreads, Cfg<FMT, NT>::kCtas)
     fence_mbar_init();
   }
 
-  // ---- this CTA's part of the sequence: `left` pairs from pair `off` of unit (item, g)
+  // ---- this CTA's part of the sequence: `left` places from place `off` of unit (item, g)
   int item, g;
   int off = 0;
   int64_t left, start = 0;
@@ -259,7 +265,7 @@ __global__ void __launch_bounds__(Cfg<FMT, NT>::kThreads, Cfg<FMT, NT>::kCtas)
     const int per = (n_items + kThreads - 1) / kThreads;
     const int i0 = min(static_cast<int>(threadIdx.x) * per, n_items), i1 = min(i0 + per, n_items);
     int64_t mine = 0, total = 0;  // an item has up to 2^26 pairs: sums in 64 bits
-    for (int i = i0; i < i1; ++i) mine += decode_item(a, i).pairs;
+    for (int i = i0; i < i1; ++i) mine += (decode_item(a, i).pairs + kUnitCost);
     int64_t incl = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -283,7 +289,7 @@ __global__ void __launch_bounds__(Cfg<FMT, NT>::kThreads, Cfg<FMT, NT>::kCtas)
     if (start >= before * H && start < (before + mine) * H) {
       int64_t at = before * H;
       for (int i = i0; i < i1; ++i) {
-        const int64_t w = static_cast<int64_t>(decode_item(a, i).pairs) * H;
+        const int64_t w = static_cast<int64_t>(decode_item(a, i).pairs + kUnitCost) * H;
         if (start < at + w) {
           ctl->item = i;
           ctl->offset = start - at;
@@ -295,14 +301,15 @@ __global__ void __launch_bounds__(Cfg<FMT, NT>::kThreads, Cfg<FMT, NT>::kCtas)
     __syncthreads();
     item = ctl->item;
     it = decode_item(a, item);
-    // the offset lies inside the item: kv heads (at most 65535) x pairs (2^26)
+    // the offset lies inside the item: kv heads (at most 65535) x places (2^26)
     const int64_t offset = ctl->offset;
+    const int places = it.pairs + kUnitCost;
     if (offset < (int64_t(1) << 31)) {
-      g = static_cast<int>(static_cast<uint32_t>(offset) / static_cast<uint32_t>(it.pairs));
+      g = static_cast<int>(static_cast<uint32_t>(offset) / static_cast<uint32_t>(places));
     } else {
-      g = static_cast<int>(offset / it.pairs);
+      g = static_cast<int>(offset / places);
     }
-    off = static_cast<int>(offset - static_cast<int64_t>(g) * it.pairs);
+    off = static_cast<int>(offset - static_cast<int64_t>(g) * places);
   } else {
     __syncthreads();
     item = blockIdx.x;
@@ -369,7 +376,7 @@ __global__ void __launch_bounds__(Cfg<FMT, NT>::kThreads, Cfg<FMT, NT>::kCtas)
         }
         go = __shfl_sync(0xffffffffu, go, 0);
       }
-      left -= end - off;
+      left -= min(static_cast<int64_t>(it.pairs + kUnitCost - off), left);
       off = 0;
       if (left > 0 && ++g == H) {
         g = 0;
@@ -390,15 +397,18 @@ __global__ void __launch_bounds__(Cfg<FMT, NT>::kThreads, Cfg<FMT, NT>::kCtas)
   const int hh = lane >> 2, c = lane & 3;
   const int G = a.group, gshift = __ffs(G) - 1;  // a power of two
   const float sl2 = a.scale_log2;
-  int64_t s = 0;            // pairs of the CTA's sequence before this unit
+  int64_t s = 0;            // places of the CTA's part before this unit
   int mine = warp;          // this warp's next pair, counted from the unit's first
   int st = warp;            // its stage and phase
   uint32_t ph = 0;
-  while (left > 0) {
+  for (;;) {
     const int first = off, end = static_cast<int>(min(static_cast<int64_t>(it.pairs), off + left));
     const int n = end - first;
-    // Q fragments and each column's row
-    uint32_t qf[NT][8][2];
+    const int64_t u0 = start + s - first;  // the unit's first place in the sequence
+    if (n > 0) {  // (else the part begins behind the unit's pairs)
+    // Q fragments and each column's row. One tile's stay in registers; two tiles' (32 registers) go to shared
+    // memory, in fragment order.
+    uint2 qf[NT == 1 ? 8 : 1];
     int row_of[NT][2];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
@@ -408,16 +418,21 @@ __global__ void __launch_bounds__(Cfg<FMT, NT>::kThreads, Cfg<FMT, NT>::kCtas)
       const uint32_t* q32 = reinterpret_cast<const uint32_t*>(
           a.q + static_cast<int64_t>(it.row0 + (live ? r : 0)) * a.q_row_stride +
           static_cast<int64_t>(g * G + (live ? col & (G - 1) : 0)) * a.q_head_stride);
+      const auto word = [&](int j, int w) {
+        const uint32_t x = live ? __ldg(q32 + (wp::q_dim<FMT>(j, w, c) >> 1)) : 0u;
+        return FMT == PBS_KV_BF16 ? x : bf16x2_to_f16x2(x);
+      };
+      if (NT == 1) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j)
-#pragma unroll
-        for (int w = 0; w < 2; ++w) {
-          const uint32_t x = live ? __ldg(q32 + (wp::q_dim<FMT>(j, w, c) >> 1)) : 0u;
-          qf[t][j][w] = FMT == PBS_KV_BF16 ? x : bf16x2_to_f16x2(x);
-        }
+        for (int j = 0; j < 8; ++j) qf[NT == 1 ? j : 0] = make_uint2(word(j, 0), word(j, 1));
+      } else {
+        for (int j = warp; j < 8; j += kWarps) ctl->q[8 * t + j][lane] = make_uint2(word(j, 0), word(j, 1));
+      }
       row_of[t][0] = (8 * t + 2 * c) >> gshift;
       row_of[t][1] = (8 * t + 2 * c + 1) >> gshift;
     }
+    if (NT > 1) consumers_sync<kWarps>();  // (the last unit's readers passed its merge)
+    const auto q_frag = [&](int t, int j) { return NT == 1 ? qf[NT == 1 ? j : 0] : ctl->q[8 * t + j][lane]; };
     float o[NT][8][4], m[NT][2], l[NT][2];
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
@@ -452,7 +467,7 @@ __global__ void __launch_bounds__(Cfg<FMT, NT>::kThreads, Cfg<FMT, NT>::kCtas)
       const uint32_t stp[kPair] = {smem_u32(stages) + st * kStage, smem_u32(stages) + st * kStage + kPage};
 
       float sc[kPair][NT][4];
-      wp::page_scores<FMT, kPair, NT>(stp, qf, lane, sc);
+      wp::page_scores<FMT, kPair, NT>(stp, q_frag, lane, sc);
       float mx[NT][2];
 #pragma unroll
       for (int t = 0; t < NT; ++t) mx[t][0] = mx[t][1] = -INFINITY;
@@ -468,7 +483,7 @@ __global__ void __launch_bounds__(Cfg<FMT, NT>::kThreads, Cfg<FMT, NT>::kCtas)
           for (int t = 0; t < NT; ++t)
 #pragma unroll
             for (int w = 0; w < 2; ++w) {
-              const uint32_t b = ((real >> i) & 1u) && row_of[t][w] < it.rows ? seen_bits(a, n0, it.p0 + row_of[t][w]) : 0u;
+              const uint32_t b = ((real >> i) & 1u) && row_of[t][w] < it.rows ? seen_bits(a, n0, it.p0 + row_of[t][w], it.p0 + row_of[t][w]) : 0u;
               if (!((b >> hh) & 1u)) sc[i][t][w] = -INFINITY;
               if (!((b >> (hh + 8)) & 1u)) sc[i][t][w + 2] = -INFINITY;
             }
@@ -527,11 +542,13 @@ __global__ void __launch_bounds__(Cfg<FMT, NT>::kThreads, Cfg<FMT, NT>::kCtas)
           wp::page_pv<FMT, NT>(stp[i], sc[i], lane, o);
         } else if ((real >> i) & 1u) {
           const int n0 = ((e < it.head ? e : e + jump) * kPair + i) * kPageRows;
-          // what every row sees is what the first row's end and the last row's window leave
+          // consecutive rows see together the last row's end of the keys and the first row's window; a key that
+          // rows between see and neither border row does cannot be (a page is as long as a group is at most)
           const int p0 = it.p0;
-          const bool same = it.rows == 1 || (seen_bits(a, n0, p0) == seen_bits(a, n0, it.p1));
-          wp::page_pv_masked<FMT, NT>(stp[i], sc[i], lane, o, same ? 1 : it.rows,
-                                      [&](int r) { return seen_bits(a, n0, p0 + r); }, row_of);
+          const uint32_t any = seen_bits(a, n0, it.p1, p0);
+          const bool same = it.rows == 1 || (any == seen_bits(a, n0, p0, p0) && any == seen_bits(a, n0, it.p1, it.p1));
+          wp::page_pv_masked<FMT, NT>(stp[i], sc[i], lane, o, any, same, it.rows,
+                                      [&](int r) { return seen_bits(a, n0, p0 + r, p0 + r); }, row_of);
         }
       }
       __syncwarp();
@@ -598,7 +615,6 @@ __global__ void __launch_bounds__(Cfg<FMT, NT>::kThreads, Cfg<FMT, NT>::kCtas)
     }
     if (!whole_unit) {
       // publish, draw a ticket; the unit's last CTA merges its parts in pair order
-      const int64_t u0 = start + s - first;  // the unit's first pair in the sequence
       const int c0 = cut.of(u0), c1 = cut.of(u0 + it.pairs - 1);
       const int64_t unit = static_cast<int64_t>(item) * H + g;
       if (threadIdx.x == 0) {  // (the warps' stores above came before the barrier: the fence covers them)
@@ -611,8 +627,10 @@ __global__ void __launch_bounds__(Cfg<FMT, NT>::kThreads, Cfg<FMT, NT>::kCtas)
         for (int col = warp; col < cols; col += kWarps) {
           // lane p holds part c0 + p's maximum and sum, 32 parts at a time
           const auto slot = [&](int c) { return a.split_ws + (2 * static_cast<int64_t>(c) + (c == c0 ? 1 : 0)) * kSlot; };
-          float M = -INFINITY;
-          for (int c = c0 + lane; c <= c1; c += 32) M = fmaxf(M, __ldcg(slot(c) + kCols * kHeadDim + col));
+          const float* s0 = slot(min(c0 + lane, c1));
+          const float m0 = __ldcg(s0 + kCols * kHeadDim + col), l0 = __ldcg(s0 + kCols * (kHeadDim + 1) + col);
+          float M = m0;
+          for (int c = c0 + 32 + lane; c <= c1; c += 32) M = fmaxf(M, __ldcg(slot(c) + kCols * kHeadDim + col));
 #pragma unroll
           for (int x = 16; x > 0; x >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, x));
           float4 O = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -621,10 +639,12 @@ __global__ void __launch_bounds__(Cfg<FMT, NT>::kThreads, Cfg<FMT, NT>::kCtas)
             const int n_parts = min(32, c1 - base + 1);
             float f = 0.f, l_of = 0.f;
             if (lane < n_parts) {
-              f = M == -INFINITY ? 1.f : ex2(__ldcg(slot(base + lane) + kCols * kHeadDim + col) - M);
-              l_of = f * __ldcg(slot(base + lane) + kCols * (kHeadDim + 1) + col);
+              const float* s = slot(base + lane);
+              const float mp = base == c0 ? m0 : __ldcg(s + kCols * kHeadDim + col);
+              f = M == -INFINITY ? 1.f : ex2(mp - M);
+              l_of = f * (base == c0 ? l0 : __ldcg(s + kCols * (kHeadDim + 1) + col));
             }
-#pragma unroll 4
+#pragma unroll 8
             for (int p = 0; p < n_parts; ++p) {
               L += __shfl_sync(0xffffffffu, l_of, p);
               add4(O, __shfl_sync(0xffffffffu, f, p),
@@ -636,10 +656,13 @@ __global__ void __launch_bounds__(Cfg<FMT, NT>::kThreads, Cfg<FMT, NT>::kCtas)
         if (threadIdx.x == 0) a.split_tickets[unit] = 0;
       }
     }
-    left -= n;
-    s += n;
+    }
+    const int64_t took = min(static_cast<int64_t>(it.pairs + kUnitCost - first), left);
+    left -= took;
+    if (left <= 0) break;
+    s += took;
     off = 0;
-    if (left > 0 && ++g == H) {
+    if (++g == H) {
       g = 0;
       it = decode_item(a, ++item);
     }

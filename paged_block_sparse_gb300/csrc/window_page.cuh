@@ -74,10 +74,10 @@ __device__ __forceinline__ int q_dim(int j, int w, int c) {
   return 32 * c + 4 * j + 2 * w;
 }
 
-// Scores of the pages at st[0..NP): s[page][tile][..]. The pages' chains interleave.
-template <int FMT, int NP, int NT>
-__device__ __forceinline__ void page_scores(const uint32_t (&st)[NP], const uint32_t (&qf)[NT][8][2], int lane,
-                                            float (&s)[NP][NT][4]) {
+// Scores of the pages at st[0..NP): s[page][tile][..]. The pages' chains interleave. q(t, j): the Q fragment of
+// tile t and k-step j.
+template <int FMT, int NP, int NT, typename Q>
+__device__ __forceinline__ void page_scores(const uint32_t (&st)[NP], Q q, int lane, float (&s)[NP][NT][4]) {
   const int hh = lane >> 2, c = lane & 3;
 #pragma unroll
   for (int i = 0; i < NP; ++i)
@@ -89,17 +89,23 @@ __device__ __forceinline__ void page_scores(const uint32_t (&st)[NP], const uint
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const int chunk = 2 * (j & 3) + hi;
+      uint2 qj[NT];
+#pragma unroll
+      for (int t = 0; t < NT; ++t) qj[t] = q(t, j);
 #pragma unroll
       for (int i = 0; i < NP; ++i) {
         uint32_t af[4];
         ldsm_x4(st[i] + line_off(key, j >> 2) + ((chunk ^ (key & 7)) << 4), af);
 #pragma unroll
-        for (int t = 0; t < NT; ++t) mma_bf16(s[i][t], af, qf[t][j][0], qf[t][j][1]);
+        for (int t = 0; t < NT; ++t) mma_bf16(s[i][t], af, qj[t].x, qj[t].y);
       }
     }
   } else if (FMT == PBS_KV_FP8_E4M3) {
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
+      uint2 qj[NT];
+#pragma unroll
+      for (int t = 0; t < NT; ++t) qj[t] = q(t, j);
 #pragma unroll
       for (int i = 0; i < NP; ++i) {
         const uint32_t w0 = lds32(st[i] + line_off(hh, 0) + ((j ^ hh) << 4) + 4 * c);
@@ -108,7 +114,7 @@ __device__ __forceinline__ void page_scores(const uint32_t (&st)[NP], const uint
         e4m3x4(w0, af[0], af[2]);
         e4m3x4(w1, af[1], af[3]);
 #pragma unroll
-        for (int t = 0; t < NT; ++t) mma_f16(s[i][t], af, qf[t][j][0], qf[t][j][1]);
+        for (int t = 0; t < NT; ++t) mma_f16(s[i][t], af, qj[t].x, qj[t].y);
       }
     }
   } else {
@@ -127,6 +133,12 @@ __device__ __forceinline__ void page_scores(const uint32_t (&st)[NP], const uint
     }
 #pragma unroll
     for (int j = 0; j < 8; j += 2) {
+      uint2 qj[2][NT];
+#pragma unroll
+      for (int t = 0; t < NT; ++t) {
+        qj[0][t] = q(t, j);
+        qj[1][t] = q(t, j + 1);
+      }
 #pragma unroll
       for (int i = 0; i < NP; ++i) {
         const uint32_t sa = j < 4 ? s0lo[i] : s0hi[i], sb = j < 4 ? s1lo[i] : s1hi[i];
@@ -137,7 +149,7 @@ __device__ __forceinline__ void page_scores(const uint32_t (&st)[NP], const uint
         for (int h = 0; h < 2; ++h) {
           uint32_t af[4] = {hmul2(a[2 * h], sa), hmul2(b[2 * h], sb), hmul2(a[2 * h + 1], sa), hmul2(b[2 * h + 1], sb)};
 #pragma unroll
-          for (int t = 0; t < NT; ++t) mma_f16(s[i][t], af, qf[t][j + h][0], qf[t][j + h][1]);
+          for (int t = 0; t < NT; ++t) mma_f16(s[i][t], af, qj[h][t].x, qj[h][t].y);
         }
       }
     }
@@ -254,18 +266,45 @@ __device__ __forceinline__ void page_pv(uint32_t st, const float (&p)[NT][4], in
   }
 }
 
-// The same for a page that the group's rows see in part. V of the keys that a row does not see is cleared in
-// registers before it meets P, since 0 * NaN is NaN: for all rows alike when they see the same keys
-// (rows == 1), else row by row, each row's product added to its own columns only. bits(r): the keys row r
-// sees; row_of: the lane's columns' rows.
+// Infinities or NaN in the words of 16-bit pairs (bf16, or f16).
+template <int FMT>
+__device__ __forceinline__ uint32_t not_finite(uint32_t x) {
+  constexpr uint32_t kExp = FMT == PBS_KV_BF16 ? 0x7f807f80u : 0x7c007c00u;
+  constexpr uint32_t kOne = FMT == PBS_KV_BF16 ? 0x00800080u : 0x04000400u;
+  return ((x & kExp) + kOne) & 0x80008000u;  // an exponent of ones carries into the sign's place
+}
+
+// The same for a page that the group's rows see in part: `any` are the keys that some row sees; `same`: every
+// row sees just those. V of the others is cleared in registers before it meets P, since 0 * NaN is NaN. Where
+// the rows differ, a key that one sees and another does not has P = 0 for the latter, which a finite V leaves at
+// 0; only when such a page holds a V that is not finite does it go row by row, each row's product added to its own
+// columns. bits(r): the keys row r sees; row_of: the lane's columns' rows.
 template <int FMT, int NT, typename Bits>
 __device__ __forceinline__ void page_pv_masked(uint32_t st, const float (&p)[NT][4], int lane, float (&o)[NT][8][4],
-                                               int rows, Bits bits, const int (&row_of)[NT][2]) {
-  const PFrag<FMT, NT> pf(p);
-  VPage<FMT> v(st, lane);
+                                               uint32_t any, bool same, int rows, Bits bits,
+                                               const int (&row_of)[NT][2]) {
+  // (each pass reads V anew: nothing but O lives across them)
+  bool finite = true;
+  if (!same) {
+    const uint2 m = key_words(any, lane & 3);
+    VPage<FMT> v(st, lane);
+    uint32_t bad = 0u;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if ((i & 3) == 0) v.begin(i >> 2);
+      uint32_t vf[4];
+      v.tile(i, vf);
+      bad |= not_finite<FMT>(vf[0] & m.x) | not_finite<FMT>(vf[1] & m.x) | not_finite<FMT>(vf[2] & m.y) |
+             not_finite<FMT>(vf[3] & m.y);
+    }
+    finite = !__any_sync(0xffffffffu, bad != 0u);
+  }
+  const int passes = finite ? 1 : rows;
 #pragma unroll 1
-  for (int r = 0; r < rows; ++r) {
-    const uint2 m = key_words(bits(r), lane & 3);
+  for (int r = 0; r < passes; ++r) {
+    const PFrag<FMT, NT> pf(p);
+    const uint2 m = key_words(finite ? any : bits(r), lane & 3);
+    VPage<FMT> v(st, lane);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       if ((i & 3) == 0) v.begin(i >> 2);
@@ -279,7 +318,7 @@ __device__ __forceinline__ void page_pv_masked(uint32_t st, const float (&p)[NT]
       for (int t = 0; t < NT; ++t) {
         float x[4] = {0.f, 0.f, 0.f, 0.f};
         pf.mma(t, x, vf);
-        const bool y0 = rows == 1 || row_of[t][0] == r, y1 = rows == 1 || row_of[t][1] == r;
+        const bool y0 = finite || row_of[t][0] == r, y1 = finite || row_of[t][1] == r;
         o[t][i][0] = y0 ? o[t][i][0] + x[0] : o[t][i][0];
         o[t][i][1] = y1 ? o[t][i][1] + x[1] : o[t][i][1];
         o[t][i][2] = y0 ? o[t][i][2] + x[2] : o[t][i][2];
