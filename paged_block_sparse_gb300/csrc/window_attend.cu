@@ -35,14 +35,13 @@ constexpr float kLazyLog2 = 8.0f;
 constexpr int kOPitch = kHeadDim + 4;  // floats: rows 4 banks apart (conflict-free partial writes)
 // CTAs per SM, consumer warps and stages per CTA. bf16 and fp8 are bound by HBM: 2 x 4 (fp8, with converts to do:
 // 2 x 5) warps keep up, 128 to 160 KiB per SM in flight. NVFP4 is bound by the pipe that converts (and compares,
-// selects and packs) at 16 lanes a clock, not by the number of warps: 32 requests of 8k-64k keys took 304 us with
-// 3 CTAs of 4 consumers, 297 with 3 of 3, 303 with 4 of 3, 367 with 2 of 7 (two producers per SM issue too
-// slowly). Two fp8 rows of 128 requests: 344 us with 2 of 5, 356 with 2 of 4, 464 with 3 of 4 and half the stages.
+// selects and packs) at 16 lanes a clock and by the chains of its warps: 32 requests of 8k-64k keys took 294 us
+// with 3 CTAs of 4 consumers, 323 with 3 of 3, 281 with 4 of 3, 357 with 2 of 7. Two fp8 rows of 128 requests: 344 us with 2 of 5, 356 with 2 of 4, 464 with 3 of 4 and half the stages.
 template <int FMT, int NT>
 struct Cfg {
-  static constexpr int kWarps = FMT == PBS_KV_FP8_E4M3 ? 5 : 4;
+  static constexpr int kWarps = FMT == PBS_KV_FP8_E4M3 ? 5 : FMT == PBS_KV_NVFP4 && NT == 1 ? 3 : 4;
   static constexpr int kStages = FMT == PBS_KV_BF16 ? 4 : 2 * kWarps;
-  static constexpr int kCtas = FMT == PBS_KV_NVFP4 && NT == 1 ? 3 : 2;
+  static constexpr int kCtas = FMT == PBS_KV_NVFP4 && NT == 1 ? 4 : 2;
   static constexpr int kThreads = 32 * (kWarps + 1);
   static_assert(kStages % kWarps == 0, "each stage must belong to one consumer warp");
 };
@@ -54,23 +53,6 @@ struct Merge {
   float m[W][8];
   float l[W][8];
 };
-
-template <int NS>
-struct Ctl {
-  uint64_t full[NS];
-  uint64_t empty[NS];
-  int32_t ok[NS];  // bit i: the stage holds page i of its pair (else padding, or not in the cache)
-  int32_t abort;
-  int32_t last;
-  int32_t item;    // where this CTA's part begins
-  int64_t offset;
-  int32_t ids[32]; // first physical page of the producer's next pairs
-  uint2 q[16][32]; // two column tiles: the unit's Q fragments, [tile * 8 + k-step][lane]
-};
-
-template <int FMT, int NT>
-constexpr size_t kSmem = 1024 + size_t(Cfg<FMT, NT>::kStages) * kPair * wp::kPageBytes<FMT> +
-                         sizeof(Merge<Cfg<FMT, NT>::kWarps>) + sizeof(Ctl<Cfg<FMT, NT>::kStages>);
 
 // One group of rows and its list of pairs.
 struct Item {
@@ -86,6 +68,24 @@ struct Item {
 // dealt out holds so many empty places behind each unit's pairs. 44 requests of up to 1.6k keys (three rows, 16
 // heads per kv head): 201 us without them, as the short requests' CTAs end last.
 constexpr int kUnitCost = 12;
+
+template <int NS>
+struct Ctl {
+  uint64_t full[NS];
+  uint64_t empty[NS];
+  int32_t ok[NS];  // bit i: the stage holds page i of its pair (else padding, or not in the cache)
+  int32_t abort;
+  int32_t last;
+  int32_t item;    // where this CTA's part begins
+  Item it;
+  int64_t offset;
+  int32_t ids[32]; // first physical page of the producer's next pairs
+  uint2 q[16][32]; // two column tiles: the unit's Q fragments, [tile * 8 + k-step][lane]
+};
+
+template <int FMT, int NT>
+constexpr size_t kSmem = 1024 + size_t(Cfg<FMT, NT>::kStages) * kPair * wp::kPageBytes<FMT> +
+                         sizeof(Merge<Cfg<FMT, NT>::kWarps>) + sizeof(Ctl<Cfg<FMT, NT>::kStages>);
 
 constexpr int kPairKeys = kPair * kPageRows;
 constexpr int kPairsPerBlock = kSparseBlock / kPairKeys;
@@ -104,7 +104,7 @@ __device__ __forceinline__ void pair_list(const WindowArgs& a, Item& it) {
 
 __device__ __forceinline__ Item decode_item(const WindowArgs& a, int item) {
   Item it;
-  it.req = item / a.groups_per_req;
+  it.req = a.groups_per_req == 1 ? item : item / a.groups_per_req;
   const int r0 = (item - it.req * a.groups_per_req) * a.rows_per_group;
   it.rows = min(a.rows_per_group, a.decode_query_len - r0);
   it.row0 = it.req * a.decode_query_len + r0;
@@ -289,9 +289,11 @@ __global__ void __launch_bounds__(Cfg<FMT, NT>::kThreads, Cfg<FMT, NT>::kCtas)
     if (start >= before * H && start < (before + mine) * H) {
       int64_t at = before * H;
       for (int i = i0; i < i1; ++i) {
-        const int64_t w = static_cast<int64_t>(decode_item(a, i).pairs + kUnitCost) * H;
+        const Item x = decode_item(a, i);
+        const int64_t w = static_cast<int64_t>(x.pairs + kUnitCost) * H;
         if (start < at + w) {
           ctl->item = i;
+          ctl->it = x;
           ctl->offset = start - at;
           break;
         }
@@ -300,7 +302,7 @@ __global__ void __launch_bounds__(Cfg<FMT, NT>::kThreads, Cfg<FMT, NT>::kCtas)
     }
     __syncthreads();
     item = ctl->item;
-    it = decode_item(a, item);
+    it = ctl->it;
     // the offset lies inside the item: kv heads (at most 65535) x places (2^26)
     const int64_t offset = ctl->offset;
     const int places = it.pairs + kUnitCost;
@@ -617,10 +619,10 @@ __global__ void __launch_bounds__(Cfg<FMT, NT>::kThreads, Cfg<FMT, NT>::kCtas)
       // publish, draw a ticket; the unit's last CTA merges its parts in pair order
       const int c0 = cut.of(u0), c1 = cut.of(u0 + it.pairs - 1);
       const int64_t unit = static_cast<int64_t>(item) * H + g;
-      if (threadIdx.x == 0) {  // (the warps' stores above came before the barrier: the fence covers them)
-        __threadfence();
-        ctl->last = atomicAdd(a.split_tickets + unit, 1) == c1 - c0;
-        __threadfence();
+      if (threadIdx.x == 0) {  // (released with the warps' stores, which came before the barrier)
+        int before;
+        asm volatile("atom.acq_rel.gpu.global.add.s32 %0, [%1], 1;" : "=r"(before) : "l"(a.split_tickets + unit) : "memory");
+        ctl->last = before == c1 - c0;
       }
       consumers_sync<kWarps>();
       if (ctl->last) {
