@@ -12,9 +12,10 @@
 //    one kv head: two 128-row MMA tiles A and B (row = token * G + head) that share every K and V block, so
 //    a block is read once per 256 rows, and the tensor cores work on one while the softmax of the other
 //    runs. Bound by the tensor pipe and, next, by the softmax warps' issue slots.
-//      warp 2     schedules: the next tile's description in one of two slots
-//      warp 0     loads: the tile's Q (tensor map), K and V images through one ring of 5 stages
-//      warp 1     issues the MMAs, in the order PV_A(i-1) S_A(i) PV_B(i-1) S_B(i)
+//      warp 2     schedules: the next tile's description in one of two slots, and its Q (tensor map)
+//      warp 0     loads: K and V images through one ring of 4 stages
+//      warp 1     issues the MMAs, in the order PV_A(n-1) S_A(n) PV_B(n-1) S_B(n) over the blocks of all its tiles
+//      warp 3     waits for the ring on warp 1's behalf
 //      warps 4-7  softmax and output of A, one thread per row; warps 8-11 of B
 //    TMEM: S_A, S_B, O_A, O_B, 128 fp32 columns each. A row's thread reads its 128 scores, writes P as fp16
 //    over the first 64 of those columns (the A operand of PV). MMAs of one thread run in issue order, so
@@ -38,7 +39,8 @@ constexpr int kThreadsTc = 384;
 constexpr int kImage = 32768;          // bytes of one K or V image
 constexpr int kHalf = kImage / 2;      // its first 64 dims
 constexpr int kQTile = kRows * kHeadDim * 2;
-constexpr int kRing = 5;
+constexpr int kRing = 4;
+constexpr int kOutStage = 8 * 4096;   // 32 rows x 64 dims of bf16 per softmax warp
 constexpr float kLazyLog2 = 8.0f;
 constexpr int kExpUp = 7, kExpDown = -8;
 constexpr unsigned long long kWaitNs = 100000000ull;
@@ -271,7 +273,7 @@ struct Tile {
 };
 
 struct Ctl {
-  uint64_t q_full, q_empty;
+  uint64_t q_full[2], q_empty[2];  // of A, of B
   uint64_t full[kRing], empty[kRing];
   uint64_t s_full[2], p_full[2];
   uint64_t pv_done[2];    // the tile's last PV
@@ -282,7 +284,7 @@ struct Ctl {
   Tile tile[2];
 };
 
-constexpr size_t kSmemTc = 2 * kQTile + kRing * kImage + sizeof(Ctl);
+constexpr size_t kSmemTc = 2 * kQTile + kRing * kImage + kOutStage + sizeof(Ctl);
 static_assert(kSmemTc <= 232448, "shared memory exceeds 227 KiB");
 constexpr uint32_t kTileUsers = 3 + 8;  // loads, MMAs, gate, the softmax warps
 
@@ -335,6 +337,19 @@ __device__ __forceinline__ int2 seen_range(const WindowArgs& a, const Tile& t, i
   return make_int2(t.head + lo - t.first, min(t.count - 1, t.head + pb / kSparseBlock - t.first));
 }
 
+// Which of the keys base .. base + 31 a row at position p sees; pages: valid bits of the two pages.
+__device__ __forceinline__ uint32_t row_bits(const WindowArgs& a, int base, int p, bool live, int pages) {
+  const int behind = p - base;
+  uint32_t w = !live || behind < 0 ? 0u : behind >= 31 ? 0xffffffffu : (2u << behind) - 1u;
+  if (a.window > 0) {
+    const int lo = p - a.window + 1 - base, s = a.num_sinks - base;
+    const uint32_t in = lo <= 0 ? 0xffffffffu : lo > 31 ? 0u : 0xffffffffu << lo;
+    const uint32_t sink = s <= 0 ? 0u : s >= 32 ? 0xffffffffu : (1u << s) - 1u;
+    w &= in | sink;
+  }
+  return w & (((pages & 1) ? 0xffffu : 0u) | ((pages & 2) ? 0xffff0000u : 0u));
+}
+
 // The last entry tile x works on (-1: none).
 __device__ __forceinline__ int last_seen(int2 r, int head) { return r.y < 0 ? -1 : r.y >= r.x ? r.y : head - 1; }
 
@@ -344,6 +359,14 @@ __device__ __forceinline__ float2 fma2(float2 x, float2 y, float2 z) {
       "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
       : "=f"(r.x), "=f"(r.y)
       : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y), "f"(z.x), "f"(z.y));
+  return r;
+}
+__device__ __forceinline__ float2 mul2(float2 x, float2 y) {
+  float2 r;
+  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmul.rn.f32x2 d, a, b;\n\t"
+      "mov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(x.x), "f"(x.y), "f"(y.x), "f"(y.y));
   return r;
 }
 __device__ __forceinline__ float2 add2(float2 x, float2 y) {
@@ -377,18 +400,19 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
   }
   uint8_t* q_s = smem;
   uint8_t* ring = smem + 2 * kQTile;
-  Ctl* ctl = reinterpret_cast<Ctl*>(ring + kRing * kImage);
+  uint8_t* out_s = ring + kRing * kImage;
+  Ctl* ctl = reinterpret_cast<Ctl*>(out_s + kOutStage);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     ctl->abort = 0;
-    mbar_init(&ctl->q_full, 1);
-    mbar_init(&ctl->q_empty, 1);
     mbar_init(&ctl->drained, 1);
     for (int i = 0; i < kRing; ++i) {
       mbar_init(&ctl->full[i], 1);
       mbar_init(&ctl->empty[i], 2);  // the MMAs and the gate
     }
     for (int i = 0; i < 2; ++i) {
+      mbar_init(&ctl->q_full[i], 1);
+      mbar_init(&ctl->q_empty[i], 1);
       mbar_init(&ctl->s_full[i], 1);
       mbar_init(&ctl->p_full[i], i == 0 ? 5 : 4);  // A's: the softmax warps and the gate
       mbar_init(&ctl->pv_done[i], 1);
@@ -416,16 +440,22 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
     int ns = 0;     // blocks of this MMA tile over the CTA's tiles
     int tiles = 0;  // tiles that had any
     bool ok = true;
-    for (int k = 0; ok; ++k) {
-      if (!warp_wait_on(&ctl->tile_full[k & 1], (k >> 1) & 1, ctl, a.err_word)) break;
-      const Tile t = ctl->tile[k & 1];
+    Tile t;
+    const auto next_tile = [&](int k) {  // false: a wait gave up
+      if (!warp_wait_on(&ctl->tile_full[k & 1], (k >> 1) & 1, ctl, a.err_word)) return false;
+      t = ctl->tile[k & 1];
       __syncwarp();
       if (lane == 0) mbar_arrive(&ctl->tile_empty[k & 1]);
-      if (t.end || aborted(ctl)) break;
+      return true;
+    };
+    ok = next_tile(0);
+    for (int k = 0; ok && !t.end && !aborted(ctl); ++k) {
       int pa, pb;
       tile_rows<kG>(t, x, &pa, &pb);
       const bool live = x * T + tok < t.n_tok;
       const int p = pa + tok;
+      // positions of the warp's rows (those without a token count: they are not written)
+      const int pw0 = pa + quad * 32 / kG, pw1 = pa + (quad * 32 + 31) / kG;
       float m = -INFINITY, l = 0.f;
       int E = 0;
       bool started = false;  // the tile has had a block: O holds something
@@ -448,26 +478,46 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
         tc::wait_ld();
         bool any = live;  // does this row see a key of the block
         if (!whole) {
-          uint32_t bits[4];
-          any = false;
+          const bool pages = (info >> 8) == 0xff;
+          const bool low_free = a.window == 0 || n0 > pb - a.window || n0 + kSparseBlock <= a.num_sinks;
+          if (pages && (low_free || (n0 >= a.num_sinks && n0 + kSparseBlock - 1 <= pa))) {
+            // One border crosses the block: the row's own position (keys j <= edge stay) or the window's far end
+            // (j >= edge). min with (edge + 1/2 - j) * inf = +-inf clears without a predicate per key.
+            const int edge = low_free ? p - n0 : p - a.window + 1 - n0;
+            const float sign = low_free ? 1.f : -1.f;
+            // (a row without a token may keep what it likes: it is not written)
+            const float at = sign * static_cast<float>(edge) + 0.5f;
+            any = live && (low_free ? edge >= 0 : edge < kSparseBlock);
+            const float2 inf = make_float2(INFINITY, INFINITY), step = make_float2(-8.f * sign, -8.f * sign);
+            // keys that every row of the warp keeps: j <= keep (j >= keep for the far end)
+            const int keep = low_free ? pw0 - n0 : pw1 - a.window + 1 - n0;
 #pragma unroll
-          for (int c = 0; c < 4; ++c) {
-            // keys 32c .. 32c + 31 of the block
-            const int base = n0 + 32 * c, behind = p - base;
-            uint32_t w = !live || behind < 0 ? 0u : behind >= 31 ? 0xffffffffu : (2u << behind) - 1u;
-            if (a.window > 0) {
-              const int lo = p - a.window + 1 - base, s = a.num_sinks - base;
-              const uint32_t in = lo <= 0 ? 0xffffffffu : lo > 31 ? 0u : 0xffffffffu << lo;
-              const uint32_t sink = s <= 0 ? 0u : s >= 32 ? 0xffffffffu : (1u << s) - 1u;
-              w &= in | sink;
+            for (int c = 0; c < 4; ++c) {
+              if (low_free ? keep >= 32 * c + 31 : keep <= 32 * c) continue;
+              float2 b[4];  // (edge + 1/2 - j) * sign for j = 32c + 0, 1 | 2, 3 | 4, 5 | 6, 7, then 8 further
+#pragma unroll
+              for (int q = 0; q < 4; ++q) b[q] = make_float2(at - sign * (32 * c + 2 * q), at - sign * (32 * c + 2 * q + 1));
+#pragma unroll
+              for (int j = 32 * c; j < 32 * c + 32; j += 8)
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                  const float2 w = mul2(b[q], inf);
+                  v[j + 2 * q] = __float_as_uint(fminf(__uint_as_float(v[j + 2 * q]), w.x));
+                  v[j + 2 * q + 1] = __float_as_uint(fminf(__uint_as_float(v[j + 2 * q + 1]), w.y));
+                  b[q] = add2(b[q], step);
+                }
             }
-            w &= (((info >> (8 + 2 * c)) & 1) ? 0xffffu : 0u) | (((info >> (9 + 2 * c)) & 1) ? 0xffff0000u : 0u);
-            bits[c] = w;
-            any |= w != 0u;
-          }
+          } else {
+            any = false;
 #pragma unroll
-          for (int j = 0; j < 128; ++j)
-            if (!(bits[j >> 5] & (1u << (j & 31)))) v[j] = 0xff800000u;  // -inf
+            for (int c = 0; c < 4; ++c) {
+              const uint32_t w = row_bits(a, n0 + 32 * c, p, live, info >> (8 + 2 * c));
+              any |= w != 0u;
+#pragma unroll
+              for (int j = 0; j < 32; ++j)
+                if (!(w & (1u << j))) v[32 * c + j] = 0xff800000u;  // -inf
+            }
+          }
         }
         float mx[4];
 #pragma unroll
@@ -540,45 +590,72 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
         ++ns;
       }
       if (!ok) break;
-      // ---- output
+      // ---- output; the next tile's description first (its S is on the way meanwhile)
+      uint8_t* stage = out_s + (warp - 4) * 4096;
+      const int rest = t.n_tok - x * T;  // the MMA tile's tokens
+      const int64_t row0 = t.t0 + x * T;
+      const int head0 = t.g * kG;
+      if (!next_tile(k + 1)) break;
       const bool blocks = __any_sync(0xffffffffu, started);
       if (blocks && !warp_wait_on(&ctl->pv_done[x], tiles++ & 1, ctl, a.err_word)) break;
       tc::fence_after_sync();
-      // O * 2^E * v_scale / l, in two steps so that no factor leaves fp32's range on its own
+      // O * 2^E * v_scale / l. The factor stays in fp32's range for |E| <= 60; beyond, 2^E goes in two steps.
       const float inv = l != 0.f ? a.v_scale / l : 0.f;
-      const float f1 = exp2i(E / 2), f2 = exp2i(E - E / 2);
-      uint16_t* dst = a.out + static_cast<int64_t>(t.t0 + x * T + tok) * a.out_row_stride +
-                      static_cast<int64_t>(t.g * kG + h) * a.out_head_stride;
+      const int e1 = max(-60, min(60, E));
+      const float f1 = inv * exp2i(e1), f2 = exp2i(E - e1);
+      const bool far = __any_sync(0xffffffffu, E != e1);
+      const bool empty = __any_sync(0xffffffffu, l == 0.f);  // a row without a key: zeros
+      // 64 dims at a time through shared memory (16-byte chunk c of row r at chunk c ^ (r % 8)), so that eight
+      // lanes write one row's 128 bytes; a thread's own row alone would cost 32 lines per store
+      const int i8 = lane >> 3;  // row 4q + i8 of the warp's 32 in store q
+      uint16_t* dst = a.out + (row0 + (quad * 32) / kG + i8 / kG) * a.out_row_stride +
+                      static_cast<int64_t>(head0 + (quad * 32) % kG + i8 % kG) * a.out_head_stride + 8 * (lane & 7);
+      const int tok0 = (quad * 32) / kG + i8 / kG;
+#pragma unroll 1
+      for (int half = 0; half < 2 && blocks; ++half) {
+        uint32_t o[64];
+        tc::ld32(to + 64 * half, *reinterpret_cast<uint32_t(*)[32]>(&o[0]));
+        tc::ld32(to + 64 * half + 32, *reinterpret_cast<uint32_t(*)[32]>(&o[32]));
+        tc::wait_ld();
+        if (far)
 #pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        uint32_t o[32];
-        if (blocks) {
-          tc::ld32(to + 32 * c, o);
-          tc::wait_ld();
-        }
-        if (live) {
+          for (int j = 0; j < 64; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * f2);
+        if (empty && l == 0.f)
 #pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            uint32_t w[4];
+          for (int j = 0; j < 64; ++j) o[j] = 0u;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const float y0 = __uint_as_float(o[8 * q + 2 * j]) * inv * f1 * f2;
-              const float y1 = __uint_as_float(o[8 * q + 2 * j + 1]) * inv * f1 * f2;
-              w[j] = l != 0.f ? pack_bf16(y0, y1) : 0u;  // no key: O was never written, or holds zeros
-            }
-            *reinterpret_cast<uint4*>(dst + 32 * c + 8 * q) = make_uint4(w[0], w[1], w[2], w[3]);
+        for (int q = 0; q < 8; ++q) {
+          uint32_t w[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            const float2 y = mul2(make_float2(__uint_as_float(o[8 * q + 2 * j]), __uint_as_float(o[8 * q + 2 * j + 1])), make_float2(f1, f1));
+            w[j] = pack_bf16(y.x, y.y);
           }
+          *reinterpret_cast<uint4*>(stage + lane * 128 + ((q ^ (lane & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
         }
+        __syncwarp();
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          const int r = 4 * q + i8;
+          const uint4 w = *reinterpret_cast<const uint4*>(stage + r * 128 + (((lane & 7) ^ (r & 7)) << 4));
+          if (tok0 + 4 * q / kG < rest)
+            *reinterpret_cast<uint4*>(dst + (4 * q / kG) * a.out_row_stride + (4 * q % kG) * a.out_head_stride + 64 * half) = w;
+        }
+        __syncwarp();
+      }
+      if (!blocks && live) {  // no block: no row of the tile sees a key
+        uint16_t* own = a.out + (row0 + tok) * a.out_row_stride + static_cast<int64_t>(head0 + h) * a.out_head_stride;
+        for (int d = 0; d < kHeadDim; d += 8) *reinterpret_cast<uint4*>(own + d) = make_uint4(0u, 0u, 0u, 0u);
       }
       if (live && a.lse != nullptr)
-        a.lse[static_cast<int64_t>(t.t0 + x * T + tok) * a.lse_row_stride + t.g * kG + h] =
-            l != 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+        a.lse[(row0 + tok) * a.lse_row_stride + head0 + h] = l != 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
       tc::fence_before_sync();
     }
   } else {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
   if (warp == 2) {
     // ------------------------------------------------------------------ scheduler
+    if (lane == 0) asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&q_map)) : "memory");
     int total = 0;  // request tiles
     for (int r0 = 0; r0 < a.num_reqs; r0 += 32) {
       int c0, p0;
@@ -586,6 +663,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
       total += __reduce_add_sync(0xffffffffu, static_cast<uint32_t>((n + 2 * T - 1) / (2 * T)));
     }
     const int flat = total * a.num_kv_heads;
+    int nq[2] = {0, 0};
     for (int k = 0;; ++k) {
       // rounds of gridDim.x tiles, from the end (a request's last tiles see the most keys), dealt in
       // alternating directions
@@ -624,14 +702,32 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
       if (lane == 0) {
         t->end = last;
         mbar_arrive(&ctl->tile_full[k & 1]);
+        // the tile's Q: A's when the last S of A of the tile before has read its own, then B's
+        for (int x = 0; !last && x < 2; ++x) {
+          if (k > 0 && !wait_on(&ctl->q_empty[x], (k - 1) & 1, ctl, a.err_word)) break;
+          if (x == 1 && t->n_tok <= T) {  // no B
+            mbar_arrive(&ctl->q_full[1]);
+            break;
+          }
+          mbar_arrive_expect_tx(&ctl->q_full[x], kQTile);
+          tma_load_3d(q_s + x * kQTile, &q_map, &ctl->q_full[x], 0, t->g * kG, t->t0 + x * T);
+          tma_load_3d(q_s + x * kQTile + kHalf, &q_map, &ctl->q_full[x], 64, t->g * kG, t->t0 + x * T);
+          ++nq[x];
+        }
       }
       __syncwarp();
-      if (last) break;
+      if (last) {
+        // every copy must land before the CTA exits
+        if (lane == 0 && k > 0) {
+          for (int x = 0; x < 2; ++x)
+            if (nq[x] > 0 && !mbar_wait_quick(&ctl->q_full[x], (k - 1) & 1, kWaitNs)) set_err(a.err_word, PBS_DEVERR_TIMEOUT);
+        }
+        break;
+      }
     }
   } else if (warp == 0) {
     // ------------------------------------------------------------------ loads
     if (lane == 0) {
-      asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&q_map)) : "memory");
       int n = 0;  // images issued
       bool go = true;
       for (int k = 0; go; ++k) {
@@ -639,13 +735,6 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
         const Tile t = ctl->tile[k & 1];
         mbar_arrive(&ctl->tile_empty[k & 1]);
         if (t.end) break;
-        if (k > 0 && !wait_on(&ctl->q_empty, (k - 1) & 1, ctl, a.err_word)) break;
-        const bool two = t.n_tok > T;
-        mbar_arrive_expect_tx(&ctl->q_full, two ? 2 * kQTile : kQTile);
-        for (int x = 0; x < (two ? 2 : 1); ++x) {
-          tma_load_3d(q_s + x * kQTile, &q_map, &ctl->q_full, 0, t.g * kG, t.t0 + x * T);
-          tma_load_3d(q_s + x * kQTile + kHalf, &q_map, &ctl->q_full, 64, t.g * kG, t.t0 + x * T);
-        }
         for (int i = 0; go && i < t.count; ++i) {
           const int b = tile_block(t, i);
           const int64_t image =
@@ -673,7 +762,22 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
     if (lane == 0) {
       int st = 0;
       uint32_t ph = 0, n = 0;
-      bool ok = true;
+      bool ok = true, pend = false;
+      auto pass = [&]() {  // the next ring entry is loaded (and not loaded again behind the gate's back)
+        if (!wait_on(&ctl->full[st], ph, ctl, a.err_word)) return false;
+        mbar_arrive(&ctl->empty[st]);
+        if (++st == kRing) {
+          st = 0;
+          ph ^= 1;
+        }
+        return true;
+      };
+      auto open = [&]() {  // A's pending PV may go; one arrival a phase
+        if (!pend) return true;
+        mbar_arrive(&ctl->p_full[0]);
+        return wait_on(&ctl->p_full[0], n++ & 1, ctl, a.err_word);
+      };
+      bool first_step = true;
       for (int k = 0; ok; ++k) {
         if (!wait_on(&ctl->tile_full[k & 1], (k >> 1) & 1, ctl, a.err_word)) break;
         const Tile* t = &ctl->tile[k & 1];
@@ -682,105 +786,125 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
         int2 r = {0, -1};
         if (!end) r = seen_range<kG>(a, *t, 0);
         mbar_arrive(&ctl->tile_empty[k & 1]);
-        if (end) break;
-        bool pend = false;
-        for (int i = 0; ok && i <= count; ++i) {
-          for (int e = i > 0 ? 0 : 1; e < (i < count ? 2 : 1); ++e) {  // V(i - 1), K(i)
-            if (!wait_on(&ctl->full[st], ph, ctl, a.err_word)) ok = false;
-            mbar_arrive(&ctl->empty[st]);  // (no stage is loaded twice behind the gate's back)
-            if (++st == kRing) {
-              st = 0;
-              ph ^= 1;
-            }
-          }
-          if (ok && pend) {
-            mbar_arrive(&ctl->p_full[0]);
-            // one arrival a phase
-            if (!wait_on(&ctl->p_full[0], n++ & 1, ctl, a.err_word)) ok = false;
-          }
-          pend = i < count && (i < head || (i >= r.x && i <= r.y)) && r.y >= 0;
+        for (int i = 0; ok && i < (end ? 1 : count); ++i) {
+          ok = (first_step || pass()) && (end || pass()) && open();  // V(n - 1), K(n)
+          first_step = false;
+          pend = r.y >= 0 && (i < head || (i >= r.x && i <= r.y));
         }
+        if (end) break;
       }
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------------ MMAs
+    // Step n of the CTA's block sequence, over its tiles: PV_A(n - 1) S_A(n) PV_B(n - 1) S_B(n). A tile's first S
+    // goes out between the last PVs of the tile before it.
     if (elect_one()) {
       constexpr uint32_t kIdescS = tc::idesc_f16(128, 128, true, false, false);
       constexpr uint32_t kIdescPV = tc::idesc_f16(128, 128, false, false, true);
       const uint64_t q_desc = tc::smem_desc_sw128(smem_u32(q_s), 16, 1024);
       const uint64_t k_desc = tc::smem_desc_sw128(smem_u32(ring), 16, 1024);
       const uint64_t v_desc = tc::smem_desc_sw128(smem_u32(ring), kHalf, 1024);
-      int st = 0;             // ring stage and phase of the next entry
+      int st = 0;             // ring stage and phase of the next entry: K(0), V(0), K(1), V(1), ..
       uint32_t ph = 0;
-      uint32_t done0 = 0, done1 = 0;  // PVs of A and of B, over the CTA's tiles
-      bool ok = true;
-      for (int k = 0; ok; ++k) {
-        if (!wait_on(&ctl->tile_full[k & 1], (k >> 1) & 1, ctl, a.err_word)) break;
-        const Tile* t = &ctl->tile[k & 1];
-        const int count = t->count, head = t->head;
-        int2 ra = {0, 0}, rb = {0, 0};
-        const bool end = t->end != 0;
+      uint32_t done[2] = {0, 0};  // PVs of A and of B
+      bool pend[2] = {false, false}, fresh[2] = {true, true}, final[2] = {false, false};
+      int k = -1, i = -1, count = 0, head = 0;  // tile, block of its list, blocks
+      int2 r[2] = {};
+      bool ok = true, end = false, first_step = true;
+      while (ok && !end) {
+        const bool next_tile = i + 1 >= count;
+        i = next_tile ? 0 : i + 1;
+        int vst = 0;
+        bool k_ready = false;
+        if (!first_step) {  // V(n - 1); with a PV of A pending, its P barrier stands for it and for K(n) (the gate)
+          vst = st;
+          k_ready = pend[0];
+          if (!pend[0] && !wait_on(&ctl->full[st], ph, ctl, a.err_word)) break;
+          if (++st == kRing) {
+            st = 0;
+            ph ^= 1;
+          }
+        }
+        const uint64_t vd = v_desc + static_cast<uint32_t>(vst * kImage >> 4);
+        const uint64_t kd = k_desc + static_cast<uint32_t>(st * kImage >> 4);
+        auto pv = [&](const int x) {  // O += P V
+          if (!pend[x]) return true;
+          if (!wait_on(&ctl->p_full[x], done[x] & 1, ctl, a.err_word)) return false;
+          tc::fence_after_sync();
+#pragma unroll
+          for (int ks = 0; ks < 8; ++ks)
+            tc::mma_ts(tmem + 256 + x * 128, tmem + x * 128 + ks * 8, vd + (ks * 2048 >> 4), kIdescPV, !(fresh[x] && ks == 0));
+          if (final[x]) tc::commit(&ctl->pv_done[x]);
+          ++done[x];
+          fresh[x] = false;
+          pend[x] = false;
+          return true;
+        };
+        auto qk = [&](const int x) {  // S = Q K^T
+          pend[x] = r[x].y >= 0 && (i < head || (i >= r[x].x && i <= r[x].y));
+          final[x] = i == last_seen(r[x], head);
+          if (pend[x]) {
+            tc::fence_after_sync();
+#pragma unroll
+            for (int ks = 0; ks < 8; ++ks) {
+              const uint32_t at = ((ks >> 2) * kHalf + (ks & 3) * 32) >> 4;
+              tc::mma_ss(tmem + x * 128, q_desc + (x * kQTile >> 4) + at, kd + at, kIdescS, ks > 0);
+            }
+            tc::commit(&ctl->s_full[x]);
+          }
+          if (i == count - 1) tc::commit(&ctl->q_empty[x]);  // the tile's last S (or none)
+        };
+        if (!next_tile) {
+          ok = pv(0) && (k_ready || wait_on(&ctl->full[st], ph, ctl, a.err_word));
+          if (!ok) break;
+          qk(0);
+          ok = pv(1);
+          if (!ok) break;
+          qk(1);
+        } else {
+          // both PVs first: S of the next tile may have to wait for its Q
+          ok = pv(0) && pv(1);
+          while (ok) {  // the next tile, skipping those without blocks
+            ++k;
+            ok = wait_on(&ctl->tile_full[k & 1], (k >> 1) & 1, ctl, a.err_word);
+            if (!ok) break;
+            const Tile* t = &ctl->tile[k & 1];
+            end = t->end != 0;
+            count = end ? 0 : t->count;
+            head = t->head;
+            if (!end) {
+              r[0] = seen_range<kG>(a, *t, 0);
+              r[1] = seen_range<kG>(a, *t, 1);
+            }
+            mbar_arrive(&ctl->tile_empty[k & 1]);
+            if (end) break;
+            ok = wait_on(&ctl->q_full[0], k & 1, ctl, a.err_word);
+            if (!ok || count > 0) break;
+            ok = wait_on(&ctl->q_full[1], k & 1, ctl, a.err_word);
+            mbar_arrive(&ctl->q_empty[0]);
+            mbar_arrive(&ctl->q_empty[1]);
+          }
+          if (!ok) break;
+          if (!end) {
+            fresh[0] = fresh[1] = true;
+            ok = k_ready || wait_on(&ctl->full[st], ph, ctl, a.err_word);
+            if (!ok) break;
+            qk(0);
+            ok = wait_on(&ctl->q_full[1], k & 1, ctl, a.err_word);
+            if (!ok) break;
+            qk(1);
+          }
+        }
+        if (!ok) break;
+        if (!first_step) tc::commit(&ctl->empty[vst]);
         if (!end) {
-          ra = seen_range<kG>(a, *t, 0);
-          rb = seen_range<kG>(a, *t, 1);
-        }
-        mbar_arrive(&ctl->tile_empty[k & 1]);
-        if (end) break;
-        if (!wait_on(&ctl->q_full, k & 1, ctl, a.err_word)) break;
-        // step i: PV of block i - 1, S of block i, of A then of B. The ring holds K(0), V(0), K(1), V(1), ..
-        bool pend0 = false, pend1 = false, fresh0 = true, fresh1 = true;
-        const int last0 = last_seen(ra, head), last1 = last_seen(rb, head);
-        for (int i = 0; i <= count; ++i) {
-          const bool has_s = i < count;
-          int vst = 0;
-          // with a PV of A pending, its P barrier stands for the step's loads too (the gate)
-          if (i > 0) {
-            vst = st;
-            if (!pend0 && !wait_on(&ctl->full[st], ph, ctl, a.err_word)) ok = false;
-            if (++st == kRing) {
-              st = 0;
-              ph ^= 1;
-            }
+          tc::commit(&ctl->empty[st]);
+          if (++st == kRing) {
+            st = 0;
+            ph ^= 1;
           }
-          if (has_s && !pend0 && !wait_on(&ctl->full[st], ph, ctl, a.err_word)) ok = false;
-          if (!ok) break;
-          const uint64_t vd = v_desc + static_cast<uint32_t>(vst * kImage >> 4);
-          const uint64_t kd = k_desc + static_cast<uint32_t>(st * kImage >> 4);
-          auto work = [&](const int x, bool& pend, bool& fresh, uint32_t& done, const int2 r, const int last) {
-            if (pend) {  // O += P V
-              if (!wait_on(&ctl->p_full[x], done & 1, ctl, a.err_word)) return false;
-              tc::fence_after_sync();
-#pragma unroll
-              for (int ks = 0; ks < 8; ++ks)
-                tc::mma_ts(tmem + 256 + x * 128, tmem + x * 128 + ks * 8, vd + (ks * 2048 >> 4), kIdescPV, !(fresh && ks == 0));
-              if (i - 1 == last) tc::commit(&ctl->pv_done[x]);
-              ++done;
-              fresh = false;
-            }
-            pend = has_s && (i < head || (i >= r.x && i <= r.y)) && r.y >= 0;
-            if (pend) {  // S = Q K^T
-              tc::fence_after_sync();
-#pragma unroll
-              for (int ks = 0; ks < 8; ++ks) {
-                const uint32_t at = ((ks >> 2) * kHalf + (ks & 3) * 32) >> 4;
-                tc::mma_ss(tmem + x * 128, q_desc + (x * kQTile >> 4) + at, kd + at, kIdescS, ks > 0);
-              }
-              tc::commit(&ctl->s_full[x]);
-            }
-            return true;
-          };
-          ok = work(0, pend0, fresh0, done0, ra, last0) && work(1, pend1, fresh1, done1, rb, last1);
-          if (!ok) break;
-          if (i > 0) tc::commit(&ctl->empty[vst]);
-          if (has_s) {
-            tc::commit(&ctl->empty[st]);
-            if (++st == kRing) {
-              st = 0;
-              ph ^= 1;
-            }
-          }
-          if (i == count - 1 || count == 0) tc::commit(&ctl->q_empty);  // the tile's last S
         }
+        first_step = false;
       }
       // every MMA must complete before TMEM is released
       tc::commit(&ctl->drained);
