@@ -280,6 +280,7 @@ struct WindowArgs {
   uint8_t* k_images;
   uint8_t* v_images;
   int32_t* image_info;
+  int32_t* next_tile;       // the attend's tile counter
   int32_t image_slots;
 };
 

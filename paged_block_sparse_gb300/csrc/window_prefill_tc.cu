@@ -202,6 +202,7 @@ __global__ void __launch_bounds__(512) convert_kernel(const WindowArgs a) {
   }
   __syncthreads();
   const int r = s_req;
+  if (t == 0 && blockIdx.x == 0 && g == 0) *a.next_tile = 0;
   if (r < 0) return;
   const int b = s_block, key = t >> 2, quarter = t & 3;
   int c0, p0;
@@ -427,9 +428,9 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
   tc::fence_after_sync();
   const uint32_t tmem = ctl->tmem;  // S_A, S_B, O_A, O_B
 
-  // the softmax warps hold a row's 128 scores in registers: 128 x 72 + 256 x 216 = the launch's 384 x 168
+  // the softmax warps hold a row's 128 scores in registers: 128 x 88 + 256 x 208 = the launch's 384 x 168
   if (warp >= 4) {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 208;");
     // ------------------------------------------------------------------ softmax and output
     const int x = (warp - 4) >> 2, quad = warp & 3;
     const int row = quad * 32 + lane;
@@ -652,7 +653,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
       tc::fence_before_sync();
     }
   } else {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
   if (warp == 2) {
     // ------------------------------------------------------------------ scheduler
     if (lane == 0) asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(&q_map)) : "memory");
@@ -665,11 +666,13 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
     const int flat = total * a.num_kv_heads;
     int nq[2] = {0, 0};
     for (int k = 0;; ++k) {
-      // rounds of gridDim.x tiles, from the end (a request's last tiles see the most keys), dealt in
-      // alternating directions
-      const int f = k * static_cast<int>(gridDim.x) + static_cast<int>((k & 1) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+      // from the end: a request's last tiles see the most keys. A CTA takes its next tile when it has room for
+      // its description (a fixed deal left 2-8 % of the CTAs' time unused)
+      int f = static_cast<int>(blockIdx.x);
       bool go = true;
       if (lane == 0 && k >= 2) go = wait_on(&ctl->tile_empty[k & 1], ((k >> 1) - 1) & 1, ctl, a.err_word);
+      if (lane == 0 && k > 0 && go) f = static_cast<int>(gridDim.x) + atomicAdd(a.next_tile, 1);
+      f = __shfl_sync(0xffffffffu, f, 0);
       go = __shfl_sync(0xffffffffu, go && !aborted(ctl), 0);
       Tile* t = &ctl->tile[k & 1];
       const bool last = !go || f >= flat;
@@ -940,7 +943,7 @@ int64_t window_image_slots(int64_t total_q, int64_t num_reqs, int64_t max_blocks
 
 size_t window_prefill_workspace(int64_t slots, int64_t num_kv_heads) {
   const int64_t images = slots * num_kv_heads;
-  return static_cast<size_t>(images) * 2 * kImage + static_cast<size_t>((images * 4 + 255) / 256 * 256);
+  return static_cast<size_t>(images) * 2 * kImage + static_cast<size_t>((images * 4 + 4 + 255) / 256 * 256);
 }
 
 void window_attach_images(WindowArgs* a, void* workspace, int64_t slots) {
@@ -949,6 +952,7 @@ void window_attach_images(WindowArgs* a, void* workspace, int64_t slots) {
   a->k_images = static_cast<uint8_t*>(workspace);
   a->v_images = a->k_images + images * kImage;
   a->image_info = reinterpret_cast<int32_t*>(a->v_images + images * kImage);
+  a->next_tile = a->image_info + images;
 }
 
 cudaError_t launch_window_prefill_tc(const WindowArgs& a, const CUtensorMap& q_map, int sms, cudaStream_t stream) {
