@@ -466,11 +466,9 @@ PBS_API size_t pbs_window_decode_workspace_bytes(int32_t batch, int32_t decode_q
  * visible keys, page table, errors and lse as in pbs_window_decode_attention. Rows at or behind
  * cu_seqlens_q[num_reqs] are left as they were (a batch padded to total_q rows).
  *   workspace    optional (NULL, 0): pbs_window_prefill_workspace_bytes() bytes or more, 256-byte
- *                aligned, no initial value; with it (and 16-byte aligned q / out rows, GQA ratios as
- *                above) the call runs on the tcgen05 kernel, otherwise on the decode kernel (mma.sync). A
+ *                aligned, no initial value; with it (and 16-byte aligned q / out rows, positive q strides and
+ *                scales) the call runs on the tcgen05 kernel, otherwise on the decode kernel (mma.sync). A
  *                smaller one is not used. Calls that share one workspace must not run concurrently.
- * On the tcgen05 kernel a key is multiplied for every token of its query tile (128 / G tokens of one
- * request): a non-finite V row reaches the tile's tokens that do not see it when a neighbour does.
  */
 PBS_API int pbs_window_prefill_attention(
     const void* q, int64_t q_row_stride, int64_t q_head_stride,

@@ -221,8 +221,9 @@ struct VPage {
   }
 };
 
-// P^T as the MMA's B operand. bf16 V: P as bf16 hi + lo (two MMAs: P keeps 16 bits); fp8 / NVFP4: V exact in
-// f16, P in f16 (2^-11).
+// P^T as the MMA's B operand. bf16 V: P as bf16 hi + lo (two MMAs: P keeps 16 bits), hi cut and lo above zero
+// where P is (by 2^-126 at least), so that an infinite V is not multiplied by a zero or by both signs; fp8 /
+// NVFP4: V exact in f16, P in f16 (2^-11).
 template <int FMT, int NT>
 struct PFrag {
   uint32_t b0[NT], b1[NT], l0[NT], l1[NT];
@@ -230,11 +231,14 @@ struct PFrag {
 #pragma unroll
     for (int t = 0; t < NT; ++t) {
       if (FMT == PBS_KV_BF16) {
-        const uint32_t h01 = pack_bf16(p[t][0], p[t][1]), h23 = pack_bf16(p[t][2], p[t][3]);
-        b0[t] = movmatrix_trans(h01);
-        b1[t] = movmatrix_trans(h23);
-        l0[t] = movmatrix_trans(pack_bf16(p[t][0] - bf16_lo(h01), p[t][1] - bf16_hi(h01)));
-        l1[t] = movmatrix_trans(pack_bf16(p[t][2] - bf16_lo(h23), p[t][3] - bf16_hi(h23)));
+        float lo[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          lo[i] = fminf(fmaxf(p[t][i] - bf16_hi(__float_as_uint(p[t][i])), 0x1p-126f), p[t][i]);
+        b0[t] = movmatrix_trans(__byte_perm(__float_as_uint(p[t][0]), __float_as_uint(p[t][1]), 0x7632));
+        b1[t] = movmatrix_trans(__byte_perm(__float_as_uint(p[t][2]), __float_as_uint(p[t][3]), 0x7632));
+        l0[t] = movmatrix_trans(pack_bf16(lo[0], lo[1]));
+        l1[t] = movmatrix_trans(pack_bf16(lo[2], lo[3]));
       } else {
         b0[t] = movmatrix_trans(pack_f16(p[t][0], p[t][1]));
         b1[t] = movmatrix_trans(pack_f16(p[t][2], p[t][3]));

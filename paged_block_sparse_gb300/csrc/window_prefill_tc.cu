@@ -44,8 +44,12 @@ constexpr int kOutStage = 8 * 4096;   // 32 rows x 64 dims of bf16 per softmax w
 constexpr float kLazyLog2 = 8.0f;
 constexpr int kExpUp = 7, kExpDown = -8;
 constexpr unsigned long long kWaitNs = 100000000ull;
-// block info word: V exponent + 128 in the low byte (0: all of V is zero), valid pages in the next
+// block info word: V exponent + 128 in the low byte (0: no finite V but zeros), valid pages in the next,
+// then whether some V is infinite or NaN
 constexpr int kInfoBias = 128;
+constexpr int kInfoOdd = 1 << 16;
+__device__ __forceinline__ int info_pages(int info) { return (info >> 8) & 0xff; }
+__device__ __forceinline__ bool finite(float x) { return fabsf(x) < INFINITY; }
 
 // What a request needs of the cache: blocks [0, head) and [first, last].
 struct Span {
@@ -184,6 +188,7 @@ __global__ void __launch_bounds__(512) convert_kernel(const WindowArgs a) {
   __shared__ int s_req, s_block;
   __shared__ float s_max[16];
   __shared__ uint32_t s_pages;
+  __shared__ int s_odd;
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31, g = blockIdx.y;
   if (warp == 0) {
     int at = 0;
@@ -191,6 +196,7 @@ __global__ void __launch_bounds__(512) convert_kernel(const WindowArgs a) {
     if (lane == 0) {
       s_req = r;
       s_pages = 0;
+      s_odd = 0;
       if (r >= 0) {
         int c0, p0;
         const int n = tokens_of(a, r, &c0, &p0);
@@ -228,6 +234,7 @@ __global__ void __launch_bounds__(512) convert_kernel(const WindowArgs a) {
   uint8_t* kdst = a.k_images + image * kImage;
   uint8_t* vdst = a.v_images + image * kImage;
   float mx = 0.f;
+  bool odd = false;
 #pragma unroll
   for (int c = 0; c < 4; ++c) {
     float v[8] = {};
@@ -238,13 +245,18 @@ __global__ void __launch_bounds__(512) convert_kernel(const WindowArgs a) {
     if (live) {
       eight<FMT>(vq, c, v);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) mx = fmaxf(mx, fabsf(v[i]) < INFINITY ? fabsf(v[i]) : 0.f);  // finite ones
+      for (int i = 0; i < 8; ++i) {
+        mx = fmaxf(mx, finite(v[i]) ? fabsf(v[i]) : 0.f);
+        odd |= !finite(v[i]);
+      }
     }
   }
 #pragma unroll
   for (int d = 1; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
   if (lane == 0) s_max[warp] = mx;
+  if (odd) s_odd = 1;
   __syncthreads();
+  odd = s_odd != 0;
 #pragma unroll
   for (int w = 0; w < 16; ++w) mx = fmaxf(mx, s_max[w]);
   int e = mx > 0.f ? static_cast<int>((__float_as_uint(mx) >> 23) & 0xffu) - 127 - 14 : 0;
@@ -254,19 +266,22 @@ __global__ void __launch_bounds__(512) convert_kernel(const WindowArgs a) {
   for (int c = 0; c < 4; ++c) {
     float v[8] = {};
     if (live) eight<FMT>(vq, c, v);
+    if (odd)  // 0 * infinity would reach the rows that do not see it: the attend adds these for those that do
+#pragma unroll
+      for (int i = 0; i < 8; ++i) v[i] = finite(v[i]) ? v[i] : 0.f;
     const int c16 = quarter * 4 + c;
     *reinterpret_cast<uint4*>(vdst + (c16 >> 3) * kHalf + key * 128 + (((c16 & 7) ^ (key & 7)) << 4)) =
         make_uint4(pack_f16(v[0] * sc, v[1] * sc), pack_f16(v[2] * sc, v[3] * sc), pack_f16(v[4] * sc, v[5] * sc),
                    pack_f16(v[6] * sc, v[7] * sc));
   }
-  if (t == 0) a.image_info[image] = (mx > 0.f ? e + kInfoBias : 0) | (static_cast<int>(s_pages) << 8);
+  if (t == 0) a.image_info[image] = (mx > 0.f ? e + kInfoBias : 0) | (static_cast<int>(s_pages) << 8) | (odd ? kInfoOdd : 0);
 }
 
 // ---- attend -------------------------------------------------------------------------------------
 
 struct Tile {
   int end;            // no tile: the list is done
-  int g, t0, n_tok;   // kv head, first row of q, tokens
+  int req, g, t0, n_tok;  // request, kv head, first row of q, tokens
   int p0;             // position of the first
   int head, first, count;
   int slot0, req_head, req_first;  // the request's first image slot, and its span: block b's slot is
@@ -390,6 +405,25 @@ __device__ __forceinline__ void ld16(uint32_t taddr, uint32_t (&v)[16]) {
       : "memory");
 }
 
+// out[d] += v_scale * V[d] where V of a key is infinite or NaN (its weight, above zero, leaves those as they are).
+template <int FMT>
+__device__ __forceinline__ void add_odd_values(const uint8_t* page, int g, int row, float v_scale, uint16_t* out) {
+#pragma unroll 1
+  for (int quarter = 0; quarter < 4; ++quarter) {
+    const Quarter<FMT> q = load_quarter<FMT>(page, g, row, 1, quarter);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      float v[8];
+      eight<FMT>(q, c, v);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        uint16_t* o = out + quarter * 32 + c * 8 + i;
+        if (!finite(v[i])) *o = static_cast<uint16_t>(pack_bf16(bf16_lo(*o) + v_scale * v[i], 0.f));
+      }
+    }
+  }
+}
+
 template <int kG>
 __global__ void __launch_bounds__(kThreadsTc, 1)
     prefill_kernel(const __grid_constant__ CUtensorMap q_map, const WindowArgs a) {
@@ -460,13 +494,15 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
       float m = -INFINITY, l = 0.f;
       int E = 0;
       bool started = false;  // the tile has had a block: O holds something
+      int odd = 0;           // kInfoOdd: one of them has infinities or NaN in V
       const int2 range = seen_range<kG>(a, t, x);
       for (int i = 0; i < t.count && range.y >= 0; ++i) {
         if (i >= t.head && (i < range.x || i > range.y)) continue;
         const int b = tile_block(t, i), n0 = b * kSparseBlock;
         const int info = __ldg(a.image_info + static_cast<int64_t>(t.slot0 + (b < t.req_head ? b : t.req_head + b - t.req_first)) *
                                                   a.num_kv_heads + t.g);
-        const bool whole = (info >> 8) == 0xff && n0 + kSparseBlock - 1 <= pa &&
+        odd |= info;
+        const bool whole = info_pages(info) == 0xff && n0 + kSparseBlock - 1 <= pa &&
                            (a.window == 0 || n0 > pb - a.window || n0 + kSparseBlock <= a.num_sinks);
         if (!warp_wait_on(&ctl->s_full[x], ns & 1, ctl, a.err_word)) {
           ok = false;
@@ -479,7 +515,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
         tc::wait_ld();
         bool any = live;  // does this row see a key of the block
         if (!whole) {
-          const bool pages = (info >> 8) == 0xff;
+          const bool pages = info_pages(info) == 0xff;
           const bool low_free = a.window == 0 || n0 > pb - a.window || n0 + kSparseBlock <= a.num_sinks;
           if (pages && (low_free || (n0 >= a.num_sinks && n0 + kSparseBlock - 1 <= pa))) {
             // One border crosses the block: the row's own position (keys j <= edge stay) or the window's far end
@@ -596,7 +632,8 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
       const int rest = t.n_tok - x * T;  // the MMA tile's tokens
       const int64_t row0 = t.t0 + x * T;
       const int head0 = t.g * kG;
-      if (!next_tile(k + 1)) break;
+      odd = (odd & kInfoOdd) != 0;
+      if (!odd && !next_tile(k + 1)) break;
       const bool blocks = __any_sync(0xffffffffu, started);
       if (blocks && !warp_wait_on(&ctl->pv_done[x], tiles++ & 1, ctl, a.err_word)) break;
       tc::fence_after_sync();
@@ -650,6 +687,36 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
       }
       if (live && a.lse != nullptr)
         a.lse[(row0 + tok) * a.lse_row_stride + head0 + h] = l != 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+      if (odd) {
+        __syncwarp();
+        uint16_t* own = a.out + (row0 + tok) * a.out_row_stride + static_cast<int64_t>(head0 + h) * a.out_head_stride;
+#pragma unroll 1
+        for (int i = 0; live && i < t.count; ++i) {
+          if (i >= t.head && (i < range.x || i > range.y)) continue;
+          const int b = tile_block(t, i);
+          const int info = __ldg(a.image_info + static_cast<int64_t>(t.slot0 + (b < t.req_head ? b : t.req_head + b - t.req_first)) *
+                                                    a.num_kv_heads + t.g);
+          if (!(info & kInfoOdd)) continue;
+          const int64_t p0 = static_cast<int64_t>(__ldg(a.page_table + static_cast<int64_t>(t.req) * a.pt_row_stride + b)) *
+                             a.block_page_stride;
+#pragma unroll 1
+          for (int c = 0; c < 4; ++c) {
+            uint32_t w = row_bits(a, b * kSparseBlock + 32 * c, p, true, info >> (8 + 2 * c));
+#pragma unroll 1
+            for (; w != 0; w &= w - 1) {
+              const int key = 32 * c + __ffs(w) - 1;
+              const uint8_t* page = a.kv_cache + (p0 + key / kPageRows) * a.page_stride_bytes;
+              switch (a.kv_dtype) {
+                case PBS_KV_BF16: add_odd_values<PBS_KV_BF16>(page, t.g, key % kPageRows, a.v_scale, own); break;
+                case PBS_KV_FP8_E4M3: add_odd_values<PBS_KV_FP8_E4M3>(page, t.g, key % kPageRows, a.v_scale, own); break;
+                default: add_odd_values<PBS_KV_NVFP4>(page, t.g, key % kPageRows, a.v_scale, own);
+              }
+            }
+          }
+        }
+        __syncwarp();
+        if (!next_tile(k + 1)) break;
+      }
       tc::fence_before_sync();
     }
   } else {
@@ -689,6 +756,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
           int c0, p0;
           const int n = tokens_of(a, r, &c0, &p0);
           const Span whole = span_of(a, p0, p0 + n - 1);
+          t->req = r;
           t->g = f % a.num_kv_heads;
           t->t0 = c0 + at * 2 * T;
           t->n_tok = min(2 * T, n - at * 2 * T);

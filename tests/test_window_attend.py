@@ -319,6 +319,43 @@ def test_prefill_bad_tables_are_reported(kv, workspace):
 
 @gpu
 @pytest.mark.parametrize("kv", FMT)
+@pytest.mark.parametrize("g", [2, 8])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (150, 20)])
+@pytest.mark.parametrize("workspace", ["auto", None])
+def test_prefill_odd_values_reach_the_rows_that_see_them(kv, g, window, sinks, workspace):
+    """Infinities and NaN in V of keys that some tokens of a tile see and others do not."""
+    c = Case(kv, 2, g, [(200, 200), (77, 390), (1, 140), (33, 33)], window, sinks, seed=g, bps=9)
+    rng = np.random.default_rng(5)
+    bits = (0x7F80, 0xFF80, 0x7FC0)  # +inf, -inf, NaN
+    for r, key in ((0, 3), (0, 60), (0, 127), (0, 128), (0, 199), (1, 10), (1, 300), (1, 389), (2, 130), (3, 32)):
+        page, row = int(c.table[r, key // 128]) * c.bps + key % 128 // 16, key % 16
+        for head in range(2):
+            if page not in c.pages or c.table[r, key // 128] < 0:
+                continue
+            for d in rng.choice(128, 3, replace=False):
+                if kv == "bf16":
+                    at = (head * 16 + row) * 512 + 256 + 2 * int(d)
+                    c.pages[page][at:at + 2] = np.array([bits[d % 3]], np.uint16).view(np.uint8)
+                elif kv == "fp8_e4m3":
+                    c.pages[page][(head * 16 + row) * 256 + 128 + int(d)] = 0x7F
+                else:
+                    c.pages[page][(2 * head + 1) * 1152 + 1024 + row * 8 + int(d) // 16] = 0x7F
+    d, e = c.dev(), err()
+    out, lse = prefill(c, d, return_lse=True, workspace=workspace, err_word=e)
+    with np.errstate(invalid="ignore"):
+        want = c.want()
+    o = want[0]
+    got = out.double().cpu().numpy()
+    assert int(e) == 0 and not np.isfinite(o).all() and np.isfinite(o).any()
+    assert np.array_equal(np.isnan(got), np.isnan(o))
+    assert np.array_equal(got == np.inf, o == np.inf) and np.array_equal(got == -np.inf, o == -np.inf)
+    ok = np.isfinite(o)
+    want[0], want[2] = np.where(ok, o, 0), np.where(ok, want[2], 0)
+    check(torch.where(torch.from_numpy(ok).cuda(), out, torch.zeros_like(out)), lse, want)
+
+
+@gpu
+@pytest.mark.parametrize("kv", FMT)
 def test_prefill_values_of_any_size(kv):
     # V blocks whose magnitudes differ by far more than fp16 spans, each the only one some rows see
     c = Case(kv, 1, 8, [(300, 300)], 20, 0, seed=12)
