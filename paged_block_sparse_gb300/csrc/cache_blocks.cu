@@ -11,6 +11,7 @@
 // kernels that fill the GPU: HBM-bound copies, kUnroll 16-byte loads in flight per thread.
 #include "pbs_device.cuh"
 #include "pbs_internal.h"
+#include "pdl.cuh"
 
 namespace pbs {
 namespace {
@@ -103,6 +104,7 @@ __device__ int take_free(bool want, int32_t* refs, int num_blocks, int* cursor, 
 __global__ void __launch_bounds__(kPlanThreads) fork_plan_kernel(const BlockArgs a) {
   __shared__ int list[kPlanThreads];
   __shared__ int warp_sums[32];
+  pdl_release();
   int cursor = 0;
   for (int i0 = 0; i0 < a.n; i0 += kPlanThreads) {
     const int i = i0 + static_cast<int>(threadIdx.x);
@@ -214,7 +216,7 @@ __device__ __forceinline__ void copy_pairs(const BlockArgs& a, const int32_t* sr
     x /= units;
     const int64_t layer = x % a.num_layers;
     const int p = static_cast<int>(x / a.num_layers);
-    const int s = __ldg(src + p), d = __ldg(dst + p);
+    const int s = src[p], d = dst[p];
     if (s < 0 || d < 0 || s == d) continue;
     if (s >= a.num_blocks || d >= a.num_blocks) {
       if (threadIdx.x == 0) set_err(a.err_word, PBS_DEVERR_BLOCK_OOB);
@@ -246,6 +248,7 @@ __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const BlockArgs a) {
 
 // Fork, second launch: the children's table rows, the shared blocks' counts, the tails' bytes.
 __global__ void __launch_bounds__(kCopyThreads) fork_apply_kernel(const BlockArgs a) {
+  pdl_wait();
   const int64_t entries = static_cast<int64_t>(a.n) * a.max_blocks;
   const int64_t step = static_cast<int64_t>(gridDim.x) * kCopyThreads;
   for (int64_t e = static_cast<int64_t>(blockIdx.x) * kCopyThreads + threadIdx.x; e < entries; e += step) {
@@ -307,6 +310,7 @@ __global__ void __launch_bounds__(kCopyThreads) release_kernel(const BlockArgs a
 // n_live (holes, ascending); there are as many of the one as of the other. copy_src / copy_dst: the
 // pairs; remap: every block's new id (-1: free).
 __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(const BlockArgs a) {
+  pdl_release();
   __shared__ int warp_sums[32];
   const int t = static_cast<int>(threadIdx.x);
   int mine = 0;
@@ -354,6 +358,7 @@ __global__ void __launch_bounds__(kPlanThreads) compact_plan_kernel(const BlockA
 }
 
 __global__ void __launch_bounds__(kCopyThreads) compact_apply_kernel(const BlockArgs a) {
+  pdl_wait();
   const int64_t step = static_cast<int64_t>(gridDim.x) * kCopyThreads;
   const int64_t t0 = static_cast<int64_t>(blockIdx.x) * kCopyThreads + threadIdx.x;
   const int moves = a.counts[1];
@@ -400,10 +405,9 @@ cudaError_t launch_reserve_blocks(const BlockArgs& a, cudaStream_t stream) {
 
 cudaError_t launch_fork(const BlockArgs& a, cudaStream_t stream) {
   fork_plan_kernel<<<1, kPlanThreads, 0, stream>>>(a);
-  cudaError_t e = cudaGetLastError();
+  const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  fork_apply_kernel<<<copy_grid(a, a.n), kCopyThreads, 0, stream>>>(a);
-  return cudaGetLastError();
+  return launch_second(fork_apply_kernel, copy_grid(a, a.n), kCopyThreads, 0, stream, a);
 }
 
 cudaError_t launch_release(const BlockArgs& a, cudaStream_t stream) {
@@ -414,10 +418,9 @@ cudaError_t launch_release(const BlockArgs& a, cudaStream_t stream) {
 
 cudaError_t launch_compact(const BlockArgs& a, cudaStream_t stream) {
   compact_plan_kernel<<<1, kPlanThreads, 0, stream>>>(a);
-  cudaError_t e = cudaGetLastError();
+  const cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  compact_apply_kernel<<<copy_grid(a, a.num_blocks / 2 + 1), kCopyThreads, 0, stream>>>(a);
-  return cudaGetLastError();
+  return launch_second(compact_apply_kernel, copy_grid(a, a.num_blocks / 2 + 1), kCopyThreads, 0, stream, a);
 }
 
 }  // namespace pbs
