@@ -938,6 +938,10 @@ int pbs_insert_index_cache(const void* index_k, int64_t k_stride0, int64_t k_str
 
 // ---- window attends --------------------------------------------------------------------------
 
+// A wider window is taken as this one: it spans any cache that the GPU's memory holds, and position - window
+// stays in 32 bits.
+constexpr int32_t kMaxWindow = 0x70000000;
+
 static int make_window_args(pbs::WindowArgs* w, const void* q, int64_t q_row_stride, int64_t q_head_stride,
                             const void* kv_cache, int64_t page_stride_bytes, int64_t num_pages, int32_t kv_dtype,
                             int32_t num_heads, int32_t num_kv_heads, int32_t head_dim, const int32_t* page_table,
@@ -973,7 +977,7 @@ static int make_window_args(pbs::WindowArgs* w, const void* q, int64_t q_row_str
   w->max_blocks = max_blocks;
   w->seq_lens = seq_lens;
   w->block_page_stride = block_page_stride;
-  w->window = window;
+  w->window = window < kMaxWindow ? window : kMaxWindow;
   w->num_sinks = num_sinks;
   w->scale_log2 = static_cast<float>(static_cast<double>(softmax_scale) * k_scale * 1.4426950408889634);
   w->v_scale = v_scale;

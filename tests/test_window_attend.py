@@ -266,6 +266,19 @@ def test_prefill_windows(kv, window, sinks):
 
 
 @gpu
+@pytest.mark.parametrize("window,sinks", [(2 ** 31 - 1, 0), (2 ** 31 - 1, 2 ** 31 - 1), (5, 2 ** 31 - 1), (0, 2 ** 31 - 1)])
+def test_widest_windows_and_sinks(window, sinks):
+    c = Case("bf16", 2, 4, [(2, 2), (2, 300), (2, 129)], 0, 0, seed=3)
+    d = c.dev()
+    c.window, c.sinks = 0, 0
+    want, plain = decode(c, d, 2, return_lse=True), prefill(c, d, return_lse=True)
+    check(*want, c.want())
+    c.window, c.sinks = window, sinks
+    for a, b in zip((*decode(c, d, 2, return_lse=True), *prefill(c, d, return_lse=True)), (*want, *plain)):
+        assert torch.equal(a, b)
+
+
+@gpu
 @pytest.mark.parametrize("kv", FMT)
 def test_prefill_long(kv):
     # sampled rows of prompts that span many key blocks and query tiles
