@@ -498,7 +498,7 @@ PBS_API size_t pbs_window_prefill_workspace_bytes(int32_t total_q, int32_t num_r
  *
  *   k, v         [num_tokens, num_kv_heads, 128] bf16, strides in elements (any; 16-byte aligned
  *                rows with unit dim stride are fastest)
- *   k_scale, v_scale  finite, not 0: bf16 stores the elements as they are and ignores them; fp8 stores
+ *   k_scale, v_scale  finite, not 0, and so their reciprocals: bf16 stores the elements as they are and ignores them; fp8 stores
  *                e4m3(x / scale), saturating; NVFP4 stores per 16 elements s = e4m3(max|x / scale| / 6) and
  *                e2m1(x / scale / s), both to nearest even, saturating (s = 0: zeros; a NaN makes its
  *                16 values NaN). The attends multiply by the same scales.

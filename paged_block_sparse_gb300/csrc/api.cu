@@ -1142,7 +1142,10 @@ int pbs_insert_kv_cache(const void* k, int64_t k_row_stride, int64_t k_head_stri
   if (kv_dtype != PBS_KV_BF16 && kv_dtype != PBS_KV_FP8_E4M3 && kv_dtype != PBS_KV_NVFP4) return PBS_ERR_ARG;
   if (num_kv_heads <= 0 || head_dim <= 0) return PBS_ERR_ARG;
   if (!std::isfinite(k_scale) || !std::isfinite(v_scale) || k_scale == 0.f || v_scale == 0.f) return PBS_ERR_ARG;
+  const float inv_k = static_cast<float>(1.0 / k_scale), inv_v = static_cast<float>(1.0 / v_scale);
+  if (!std::isfinite(inv_k) || !std::isfinite(inv_v)) return PBS_ERR_ARG;
   if (head_dim != kHeadDim || num_kv_heads > 65535) return PBS_ERR_UNSUPPORTED;
+  if (static_cast<int64_t>(num_tokens) * num_kv_heads > (int64_t(1) << 33)) return PBS_ERR_UNSUPPORTED;  // the grid
   if (k_row_stride < 0 || k_head_stride < 0 || k_dim_stride < 0 || v_row_stride < 0 || v_head_stride < 0 ||
       v_dim_stride < 0 || slot_stride < 0 || block_page_stride < kBlockPages)
     return PBS_ERR_SHAPE;
@@ -1168,8 +1171,8 @@ int pbs_insert_kv_cache(const void* k, int64_t k_row_stride, int64_t k_head_stri
   a.block_page_stride = block_page_stride;
   a.slot_mapping = slot_mapping;
   a.slot_stride = slot_stride;
-  a.inv_k_scale = static_cast<float>(1.0 / k_scale);
-  a.inv_v_scale = static_cast<float>(1.0 / v_scale);
+  a.inv_k_scale = inv_k;
+  a.inv_v_scale = inv_v;
   a.err_word = err_word;
   return pbs::launch_kv_insert(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? PBS_OK : PBS_ERR_CUDA;
 }

@@ -45,6 +45,11 @@ def test_insert_refusals(L, want, kw):
     assert L.pbs_insert_kv_cache(*a.values(), N, N) == want
 
 
+@pytest.mark.parametrize("want,kw", [(1, dict(ks=1e-39)), (1, dict(vs=-1e-39)), (3, dict(n=2 ** 31 - 1, h=65535))])
+def test_insert_refuses_scales_without_a_reciprocal_and_grids_past_31_bits(L, want, kw):
+    test_insert_refusals(L, want, kw)
+
+
 POOL = dict(kv=A, ls=0, nl=1, ps=64, pb=64, np=64, bps=8)
 ROWS = dict(pt=A, pts=4, nr=3, mb=4)
 
