@@ -464,7 +464,8 @@ PBS_API size_t pbs_window_decode_workspace_bytes(int32_t batch, int32_t decode_q
 /*
  * Window attend with sinks, varlen prefill: token positions as in pbs_sparse_prefill_attention, the
  * visible keys, page table, errors and lse as in pbs_window_decode_attention. Rows at or behind
- * cu_seqlens_q[num_reqs] are left as they were (a batch padded to total_q rows).
+ * cu_seqlens_q[num_reqs] are left as they were (a batch padded to total_q rows). Requests whose rows start
+ * before 0 are left out; where cu_seqlens_q decreases, rows may get zeros (PBS_DEVERR_TABLE).
  *   workspace    optional (NULL, 0): pbs_window_prefill_workspace_bytes() bytes or more, 256-byte
  *                aligned, no initial value; with it (and 16-byte aligned q / out rows, positive q strides and
  *                scales) the call runs on the tcgen05 kernel, otherwise on the decode kernel (mma.sync). A

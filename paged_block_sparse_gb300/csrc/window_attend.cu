@@ -123,7 +123,7 @@ __device__ __forceinline__ Item prefill_item(const WindowArgs& a, int item, int 
     const int r = r0 + lane;
     const int c0 = r < a.num_reqs ? __ldg(a.cu_seqlens_q + r) : 0;
     const int n = r < a.num_reqs ? __ldg(a.cu_seqlens_q + r + 1) - c0 : 0;
-    const int groups = n > 0 ? (n + a.rows_per_group - 1) / a.rows_per_group : 0;
+    const int groups = n > 0 && c0 >= 0 ? (n + a.rows_per_group - 1) / a.rows_per_group : 0;
     int incl = groups;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {

@@ -74,7 +74,7 @@ __device__ __forceinline__ int tokens_of(const WindowArgs& a, int r, int* c0, in
   *c0 = __ldg(a.cu_seqlens_q + r);
   const int n = __ldg(a.cu_seqlens_q + r + 1) - *c0;
   *p0 = __ldg(a.seq_lens + r) - n;
-  return max(0, min(n, a.num_rows - *c0));
+  return *c0 < 0 ? 0 : max(0, min(n, a.num_rows - *c0));
 }
 
 // The request that holds entry `index` when request r has count(r) entries, in order; `at` its entry there.
@@ -762,9 +762,11 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
           t->n_tok = min(2 * T, n - at * 2 * T);
           t->p0 = p0 + at * 2 * T;
           const Span s = span_of(a, t->p0, t->p0 + t->n_tok - 1);
+          const bool held = slot0 >= 0 && slot0 + whole.count <= a.image_slots;  // always, if cu_seqlens_q does not decrease
+          if (!held) set_err(a.err_word, PBS_DEVERR_TABLE);
           t->head = s.head;
           t->first = s.first;
-          t->count = s.count;
+          t->count = held ? s.count : 0;
           t->slot0 = slot0;
           t->req_head = whole.head;
           t->req_first = whole.first;

@@ -311,6 +311,18 @@ def test_prefill_padded_rows_and_strides(workspace):
 
 
 @gpu
+@pytest.mark.parametrize("workspace", ["auto", None])
+def test_prefill_requests_that_start_before_row_0_are_left_out(workspace):
+    c = Case("bf16", 2, 4, [(8, 50), (7, 200)], 40, 3, seed=8)
+    d = c.dev()
+    out = torch.full_like(d["q"], 7.0)
+    d["cu"][0] = -3
+    prefill(c, d, out=out, workspace=workspace)
+    assert (out[:8] == 7.0).all()
+    check(out, None, c.want(range(8, 15)), range(8, 15))
+
+
+@gpu
 @pytest.mark.parametrize("kv", FMT)
 @pytest.mark.parametrize("workspace", ["auto", None])
 def test_prefill_bad_tables_are_reported(kv, workspace):
