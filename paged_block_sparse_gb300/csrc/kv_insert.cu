@@ -13,7 +13,8 @@
 // An HBM copy with a few conversions per element: one warp per (token, kv heads in chunks of
 // kHeads), lanes 0-15 hold K and 16-31 V, 8 elements (16 bytes of bf16) each, so a head's row is
 // one 512-byte read per side and one 512 / 256 / 2 x 64-byte write. kHeads heads per warp are
-// loaded before the first is converted (bytes in flight).
+// loaded before the first is converted (bytes in flight). Measured: 22528 tokens x 8 heads to fp8
+// (139 MB) 20.4 us on the device = the copy rate, 24.6 us a call; 64 tokens 5 us.
 #include "pbs_device.cuh"
 #include "pbs_internal.h"
 
