@@ -12,6 +12,7 @@ Sources (vLLM API pages): ``vllm.models.minimax_m3.nvidia.sparse_attention_flash
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -667,6 +668,13 @@ def window_prefill_workspace_bytes(total_q: int, num_reqs: int, num_kv_heads: in
                                                         int(num_sinks)))
 
 
+@functools.lru_cache(maxsize=512)
+def _decode_workspace_need(device, *shape):
+    """pbs_window_decode_workspace_bytes on `device` (it depends on the number of SMs)."""
+    with torch.cuda.device(device):
+        return int(lib().pbs_window_decode_workspace_bytes(*shape))
+
+
 def _window_workspace(kind, need, device, stream):
     """The cached workspace of (kind, device, stream), grown on demand. Calls on one stream run in
     order, so they may share it; a call under graph capture gets memory of the graph's own, so that
@@ -729,7 +737,7 @@ def window_decode_attention(q, kv_cache, kv_dtype: str, num_kv_heads: int, page_
     if isinstance(workspace, str):
         if workspace != "auto":
             raise ValueError('workspace must be "auto", None or a uint8 CUDA tensor')
-        need = int(L.pbs_window_decode_workspace_bytes(batch, dql, hq, hkv))
+        need = _decode_workspace_need(dev, batch, dql, hq, hkv)
         workspace = _window_workspace("decode", need, dev, stream) if need else None
     wp, wb = (None, 0) if workspace is None else (_vec(workspace, "workspace", dev, torch.uint8), workspace.numel())
     _call(dev, L.pbs_window_decode_attention, "pbs_window_decode_attention",

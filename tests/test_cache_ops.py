@@ -565,3 +565,58 @@ def test_a_servers_life(kv):
     look([0, 1, 2, 3])
     pbs.release_cache_blocks(table, lens, refs, i32([0, 1, 2, 3]), err_word=e)
     assert not bool(refs.any()) and not bool((table >= 0).any()) and int(e) == 0
+
+
+@gpu
+@pytest.mark.parametrize("how", ["stream", "graph"])
+def test_cache_operations_on_another_stream_and_in_a_graph(how):
+    """Reserve, insert, fork, copy, a window's release and compact as one sequence: the same state as on the
+    current stream, each time the graph is replayed."""
+    hkv, nb, rows, width = 2, 300, 40, 12
+    rng = np.random.default_rng(2)
+    first = i32(list(range(8))), i32(rng.integers(100, 1400, 8).tolist())
+    grow = i32(list(range(16))), i32(rng.integers(1, 3, 16).tolist())
+    src, dst = i32([i % 8 for i in range(16)]), i32(list(range(8, 24)))
+    k = torch.randn(64, hkv, 128, device="cuda").to(torch.bfloat16)
+    slots = torch.from_numpy(rng.permutation(nb * 128)[:64]).cuda()
+    moved = i32([290, 291]), i32([298, 299])
+
+    def state():
+        gen = torch.Generator(device="cuda").manual_seed(1)
+        cache = torch.randint(0, 256, (nb * 8, page_bytes("fp8_e4m3", hkv)), dtype=torch.uint8, device="cuda", generator=gen)
+        return cache, torch.full((rows, width), -1, dtype=torch.int32, device="cuda"), i32([0] * rows), i32([0] * nb)
+
+    def sequence(s, **kw):
+        cache, table, lens, refs = s
+        pbs.reserve_cache_blocks(table, lens, refs, *first, **kw)
+        pbs.insert_kv_cache(k, k, cache, "fp8_e4m3", slots, 0.5, 0.25, **kw)
+        pairs = pbs.fork_cache(cache, table, lens, refs, src, dst, **kw)
+        pbs.reserve_cache_blocks(table, lens, refs, *grow, **kw)
+        pbs.copy_cache_blocks(cache, *moved, **kw)
+        pbs.release_cache_blocks(table, lens, refs, first[0], **kw)
+        pbs.release_cache_blocks(table, lens, refs, dst, window=200, num_sinks=3, **kw)
+        return (*pairs, *pbs.compact_cache(cache, table, refs, **kw))
+
+    want = state()
+    out = sequence(want)
+    s = state()
+    start = [x.clone() for x in s]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    if how == "stream":
+        got = sequence(s, stream=side)
+        side.synchronize()
+        runs = 1
+    else:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            got = sequence(s)
+        runs = 3
+    for _ in range(runs):
+        if how == "graph":
+            for x, y in zip(s, start):
+                x.copy_(y)
+            graph.replay()
+        torch.cuda.synchronize()
+        for a, b in zip((*want, *out), (*s, *got)):
+            assert torch.equal(a, b)

@@ -425,3 +425,28 @@ def test_window_and_sparse_attends_agree(kv):
                                              c.scale, c.k_scale, c.v_scale, return_lse=True)
     check(ours, l1, c.want())
     check(theirs, l2, c.want())
+
+
+@gpu
+@pytest.mark.parametrize("kv", FMT)
+def test_prefill_calls_on_two_streams_at_once(kv):
+    cases = [Case(kv, 2, 4, [(300, 300), (70, 500)], 130, 20, seed=21), Case(kv, 2, 4, [(520, 700)], 0, 0, seed=22)]
+    ds = [c.dev() for c in cases]
+    want = [prefill(c, d, return_lse=True) for c, d in zip(cases, ds)]
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    got = [[prefill(c, d, return_lse=True, stream=st) for c, d, st in zip(cases, ds, streams)] for _ in range(5)]
+    torch.cuda.synchronize()
+    for pair in got:
+        for a, b in zip(pair, want):
+            assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+@gpu
+def test_empty_calls_leave_nothing_behind():
+    c = Case("bf16", 2, 4, [(2, 40)], 16, 2)
+    d = c.dev()
+    none = dict(d, q=d["q"][:0], table=d["table"][:0], lens=d["lens"][:0])
+    assert decode(c, none, 2).shape == (0, 8, 128)
+    out = prefill(c, dict(d, q=d["q"][:0], cu=torch.zeros(2, dtype=torch.int32, device="cuda")))
+    assert out.shape == (0, 8, 128)
