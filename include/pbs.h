@@ -468,8 +468,9 @@ PBS_API size_t pbs_window_decode_workspace_bytes(int32_t batch, int32_t decode_q
  * before 0 are left out; where cu_seqlens_q decreases, rows may get zeros (PBS_DEVERR_TABLE).
  *   workspace    optional (NULL, 0): pbs_window_prefill_workspace_bytes() bytes or more, 256-byte
  *                aligned, no initial value; with it (and 16-byte aligned q / out rows, positive q strides and
- *                scales) the call runs on the tcgen05 kernel, otherwise on the decode kernel (mma.sync). A
- *                smaller one is not used. Calls that share one workspace must not run concurrently.
+ *                scales) the call runs on the tcgen05 kernel, otherwise on the decode kernel (mma.sync). With
+ *                less it takes the requests in parts, as many at a time as it holds (the size that the query
+ *                gives for them); less than one request's is not used. Calls that share one workspace must not run concurrently.
  */
 PBS_API int pbs_window_prefill_attention(
     const void* q, int64_t q_row_stride, int64_t q_head_stride,

@@ -652,6 +652,8 @@ def _table(t, name, device):
 
 
 _window_workspaces: dict = {}
+# "auto" gives a window prefill call no more (the call then takes its requests in parts)
+WINDOW_WORKSPACE_CAP = 8 << 30
 
 
 def window_decode_workspace_bytes(batch: int, decode_query_len: int, num_heads: int, num_kv_heads: int) -> int:
@@ -756,8 +758,8 @@ def window_prefill_attention(q, kv_cache, kv_dtype: str, num_kv_heads: int, page
                              stream=None, workspace="auto", lse=None, return_lse: bool = False):
     """:func:`window_decode_attention`'s rule for the tokens of varlen prefill requests (positions as
     in :func:`sparse_prefill_attention`). Rows of q behind cu_seqlens_q[-1] are left as they were in
-    ``out``. ``workspace``: "auto", None (the mma.sync kernel) or a uint8 tensor of
-    :func:`window_prefill_workspace_bytes` bytes."""
+    ``out``. ``workspace``: "auto" (up to ``WINDOW_WORKSPACE_CAP`` bytes), None (the mma.sync kernel) or a
+    uint8 tensor of :func:`window_prefill_workspace_bytes` bytes for all requests or for some at a time."""
     dev, pt, out, lse = _window_prologue(q, kv_cache, kv_dtype, page_table, seq_lens, out, lse, return_lse, stream)
     L = lib()
     reqs, hkv = seq_lens.shape[0], int(num_kv_heads)
@@ -768,6 +770,9 @@ def window_prefill_attention(q, kv_cache, kv_dtype: str, num_kv_heads: int, page
             raise ValueError('workspace must be "auto", None or a uint8 CUDA tensor')
         need = int(L.pbs_window_prefill_workspace_bytes(q.shape[0], reqs, hkv, pt.shape[1], KV_DTYPES[kv_dtype],
                                                         int(window), int(num_sinks)))
+        if need > WINDOW_WORKSPACE_CAP:
+            one = window_prefill_workspace_bytes(q.shape[0], 1, hkv, pt.shape[1], kv_dtype, window, num_sinks)
+            need = WINDOW_WORKSPACE_CAP if one <= WINDOW_WORKSPACE_CAP else 0
         workspace = _window_workspace("prefill", need, dev, stream) if need else None
     wp, wb = (None, 0) if workspace is None else (_vec(workspace, "workspace", dev, torch.uint8), workspace.numel())
     _call(dev, L.pbs_window_prefill_attention, "pbs_window_prefill_attention",

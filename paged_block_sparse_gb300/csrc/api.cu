@@ -1102,18 +1102,29 @@ int pbs_window_prefill_attention(const void* q, int64_t q_row_stride, int64_t q_
   w.decode_query_len = 1;
   // the tcgen05 kernel: its workspace, rows that a tensor map and 16-byte stores can address, and a
   // positive scale (its row maximum is taken before the scale)
-  const int64_t slots = pbs::window_image_slots(total_q, num_reqs, max_blocks, window, num_sinks);
-  if (workspace != nullptr && aligned(workspace, 256) &&
-      workspace_bytes >= pbs::window_prefill_workspace(slots, num_kv_heads) && slots <= 0x7fffffff && w.scale_log2 > 0.f &&
-      aligned(q, 16) && aligned(out, 16) && q_row_stride > 0 && q_head_stride > 0 && q_row_stride % 8 == 0 &&
-      q_head_stride % 8 == 0 && out_row_stride % 8 == 0 && out_head_stride % 8 == 0) {
+  // (as many requests at a time as it holds the images of, halved until they fit)
+  const auto slots_of = [&](int32_t n) { return pbs::window_image_slots(total_q, n, max_blocks, window, num_sinks); };
+  const auto held = [&](int32_t n) {
+    return slots_of(n) <= 0x7fffffff && workspace_bytes >= pbs::window_prefill_workspace(slots_of(n), num_kv_heads);
+  };
+  int32_t per = num_reqs;
+  while (per > 1 && !held(per)) per = (per + 1) / 2;
+  if (workspace != nullptr && aligned(workspace, 256) && held(per) && w.scale_log2 > 0.f && aligned(q, 16) &&
+      aligned(out, 16) && q_row_stride > 0 && q_head_stride > 0 && q_row_stride % 8 == 0 && q_head_stride % 8 == 0 &&
+      out_row_stride % 8 == 0 && out_head_stride % 8 == 0) {
     CUtensorMap q_map;
     st = encode_q_map(&q_map, q, num_heads, w.group, total_q, q_row_stride, q_head_stride);
     if (st != PBS_OK) return st;
-    pbs::window_attach_images(&w, workspace, slots);
-    return pbs::launch_window_prefill_tc(w, q_map, num_sms(), reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess
-               ? PBS_OK
-               : PBS_ERR_CUDA;
+    for (int64_t r0 = 0; r0 < num_reqs; r0 += per) {
+      w.num_reqs = num_reqs - r0 < per ? static_cast<int32_t>(num_reqs - r0) : per;
+      w.page_table = page_table + r0 * pt_row_stride;
+      w.cu_seqlens_q = cu_seqlens_q + r0;
+      w.seq_lens = seq_lens + r0;
+      pbs::window_attach_images(&w, workspace, slots_of(w.num_reqs));
+      if (pbs::launch_window_prefill_tc(w, q_map, num_sms(), reinterpret_cast<cudaStream_t>(stream)) != cudaSuccess)
+        return PBS_ERR_CUDA;
+    }
+    return PBS_OK;
   }
   pbs::window_geometry(&w, 16);
   return launch_window(w, num_sms(), stream);

@@ -57,6 +57,7 @@ constexpr unsigned long long kWaitNs = 100000000ull;
 // block info word: V exponent + 128 in the low byte (0: no finite V but zeros), valid pages in the next,
 // then whether some V is infinite or NaN
 constexpr int kInfoBias = 128;
+constexpr int kMaxConvertCtas = 16384;  // 27 waves of the GPU: no call pays for more empty slots than that
 constexpr int kInfoOdd = 1 << 16;
 __device__ __forceinline__ int info_pages(int info) { return (info >> 8) & 0xff; }
 __device__ __forceinline__ bool finite(float x) { return fabsf(x) < INFINITY; }
@@ -192,7 +193,8 @@ __device__ __forceinline__ void eight(const Quarter<FMT>& q, int c, float (&v)[8
 }
 
 // CTA (slot, kv head), 512 threads: thread t converts dims 32 (t % 4) .. of key t / 4, so that a warp reads
-// whole rows of eight keys.
+// whole rows of eight keys. The slots in use come first; a page table far wider than its requests has many that
+// are not, so a CTA of a large grid takes every gridDim.x-th slot until it meets one.
 template <int FMT>
 __global__ void __launch_bounds__(512) convert_kernel(const WindowArgs a) {
   __shared__ int s_req, s_block;
@@ -200,91 +202,94 @@ __global__ void __launch_bounds__(512) convert_kernel(const WindowArgs a) {
   __shared__ uint32_t s_pages;
   __shared__ int s_odd;
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31, g = blockIdx.y;
-  if (warp == 0) {
-    int at = 0;
-    const int r = find_request(a, blockIdx.x, lane, &at, [&](int i) { return blocks_of(a, i); });
-    if (lane == 0) {
-      s_req = r;
-      s_pages = 0;
-      s_odd = 0;
-      if (r >= 0) {
-        int c0, p0;
-        const int n = tokens_of(a, r, &c0, &p0);
-        const Span s = span_of(a, p0, p0 + n - 1);
-        s_block = at < s.head ? at : s.first + at - s.head;
-        if (at == 0 && (p0 + n - 1) / kSparseBlock >= a.max_blocks) set_err(a.err_word, PBS_DEVERR_BLOCK_OOB);
-      }
-    }
-  }
-  __syncthreads();
-  const int r = s_req;
   if (t == 0 && blockIdx.x == 0 && g == 0) *a.next_tile = 0;
-  if (r < 0) return;
-  const int b = s_block, key = t >> 2, quarter = t & 3;
-  int c0, p0;
-  const int n_tok = tokens_of(a, r, &c0, &p0);
-  const int n = b * kSparseBlock + key;
-  bool live = n < p0 + n_tok && (a.window == 0 || n > max(p0, 0) - a.window || n < a.num_sinks);
-  const uint8_t* page = a.kv_cache;
-  const int phys = __ldg(a.page_table + static_cast<int64_t>(r) * a.pt_row_stride + b);
-  const int64_t p = static_cast<int64_t>(phys) * a.block_page_stride + key / kPageRows;
-  if (phys < 0 || p >= a.num_pages) {
-    if (live) set_err(a.err_word, PBS_DEVERR_PAGE_OOB);
-    live = false;
-  } else {
-    page += p * a.page_stride_bytes;
-    if (t % 64 == 0) atomicOr(&s_pages, 1u << (key / kPageRows));
-  }
-  Quarter<FMT> kq, vq;
-  if (live) {
-    kq = load_quarter<FMT>(page, g, key % kPageRows, 0, quarter);
-    vq = load_quarter<FMT>(page, g, key % kPageRows, 1, quarter);
-  }
-  const int64_t image = static_cast<int64_t>(blockIdx.x) * a.num_kv_heads + g;
-  uint8_t* kdst = a.k_images + image * kImage;
-  uint8_t* vdst = a.v_images + image * kImage;
-  float mx = 0.f;
-  bool odd = false;
-#pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    float v[8] = {};
-    if (live) eight<FMT>(kq, c, v);
-    const int c16 = quarter * 4 + c;  // 16-byte chunk of the key's 256 bytes
-    *reinterpret_cast<uint4*>(kdst + (c16 >> 3) * kHalf + key * 128 + (((c16 & 7) ^ (key & 7)) << 4)) =
-        make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
-    if (live) {
-      eight<FMT>(vq, c, v);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        mx = fmaxf(mx, finite(v[i]) ? fabsf(v[i]) : 0.f);
-        odd |= !finite(v[i]);
+  for (int slot = blockIdx.x; slot < a.image_slots; slot += gridDim.x) {
+    if (warp == 0) {
+      int at = 0;
+      const int r = find_request(a, slot, lane, &at, [&](int i) { return blocks_of(a, i); });
+      if (lane == 0) {
+        s_req = r;
+        s_pages = 0;
+        s_odd = 0;
+        if (r >= 0) {
+          int c0, p0;
+          const int n = tokens_of(a, r, &c0, &p0);
+          const Span s = span_of(a, p0, p0 + n - 1);
+          s_block = at < s.head ? at : s.first + at - s.head;
+          if (at == 0 && (p0 + n - 1) / kSparseBlock >= a.max_blocks) set_err(a.err_word, PBS_DEVERR_BLOCK_OOB);
+        }
       }
     }
+    __syncthreads();
+    const int r = s_req;
+    if (r < 0) return;
+    const int b = s_block, key = t >> 2, quarter = t & 3;
+    int c0, p0;
+    const int n_tok = tokens_of(a, r, &c0, &p0);
+    const int n = b * kSparseBlock + key;
+    bool live = n < p0 + n_tok && (a.window == 0 || n > max(p0, 0) - a.window || n < a.num_sinks);
+    const uint8_t* page = a.kv_cache;
+    const int phys = __ldg(a.page_table + static_cast<int64_t>(r) * a.pt_row_stride + b);
+    const int64_t p = static_cast<int64_t>(phys) * a.block_page_stride + key / kPageRows;
+    if (phys < 0 || p >= a.num_pages) {
+      if (live) set_err(a.err_word, PBS_DEVERR_PAGE_OOB);
+      live = false;
+    } else {
+      page += p * a.page_stride_bytes;
+      if (t % 64 == 0) atomicOr(&s_pages, 1u << (key / kPageRows));
+    }
+    Quarter<FMT> kq, vq;
+    if (live) {
+      kq = load_quarter<FMT>(page, g, key % kPageRows, 0, quarter);
+      vq = load_quarter<FMT>(page, g, key % kPageRows, 1, quarter);
+    }
+    const int64_t image = static_cast<int64_t>(slot) * a.num_kv_heads + g;
+    uint8_t* kdst = a.k_images + image * kImage;
+    uint8_t* vdst = a.v_images + image * kImage;
+    float mx = 0.f;
+    bool odd = false;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      float v[8] = {};
+      if (live) eight<FMT>(kq, c, v);
+      const int c16 = quarter * 4 + c;  // 16-byte chunk of the key's 256 bytes
+      *reinterpret_cast<uint4*>(kdst + (c16 >> 3) * kHalf + key * 128 + (((c16 & 7) ^ (key & 7)) << 4)) =
+          make_uint4(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]), pack_bf16(v[6], v[7]));
+      if (live) {
+        eight<FMT>(vq, c, v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          mx = fmaxf(mx, finite(v[i]) ? fabsf(v[i]) : 0.f);
+          odd |= !finite(v[i]);
+        }
+      }
+    }
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+    if (lane == 0) s_max[warp] = mx;
+    if (odd) s_odd = 1;
+    __syncthreads();
+    odd = s_odd != 0;
+#pragma unroll
+    for (int w = 0; w < 16; ++w) mx = fmaxf(mx, s_max[w]);
+    int e = mx > 0.f ? static_cast<int>((__float_as_uint(mx) >> 23) & 0xffu) - 127 - 14 : 0;
+    e = max(-100, min(100, e));
+    const float sc = exp2i(-e);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      float v[8] = {};
+      if (live) eight<FMT>(vq, c, v);
+      if (odd)  // 0 * infinity would reach the rows that do not see it: the attend adds these for those that do
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[i] = finite(v[i]) ? v[i] : 0.f;
+      const int c16 = quarter * 4 + c;
+      *reinterpret_cast<uint4*>(vdst + (c16 >> 3) * kHalf + key * 128 + (((c16 & 7) ^ (key & 7)) << 4)) =
+          make_uint4(pack_f16(v[0] * sc, v[1] * sc), pack_f16(v[2] * sc, v[3] * sc), pack_f16(v[4] * sc, v[5] * sc),
+                     pack_f16(v[6] * sc, v[7] * sc));
+    }
+    if (t == 0) a.image_info[image] = (mx > 0.f ? e + kInfoBias : 0) | (static_cast<int>(s_pages) << 8) | (odd ? kInfoOdd : 0);
+    __syncthreads();
   }
-#pragma unroll
-  for (int d = 1; d < 32; d <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
-  if (lane == 0) s_max[warp] = mx;
-  if (odd) s_odd = 1;
-  __syncthreads();
-  odd = s_odd != 0;
-#pragma unroll
-  for (int w = 0; w < 16; ++w) mx = fmaxf(mx, s_max[w]);
-  int e = mx > 0.f ? static_cast<int>((__float_as_uint(mx) >> 23) & 0xffu) - 127 - 14 : 0;
-  e = max(-100, min(100, e));
-  const float sc = exp2i(-e);
-#pragma unroll
-  for (int c = 0; c < 4; ++c) {
-    float v[8] = {};
-    if (live) eight<FMT>(vq, c, v);
-    if (odd)  // 0 * infinity would reach the rows that do not see it: the attend adds these for those that do
-#pragma unroll
-      for (int i = 0; i < 8; ++i) v[i] = finite(v[i]) ? v[i] : 0.f;
-    const int c16 = quarter * 4 + c;
-    *reinterpret_cast<uint4*>(vdst + (c16 >> 3) * kHalf + key * 128 + (((c16 & 7) ^ (key & 7)) << 4)) =
-        make_uint4(pack_f16(v[0] * sc, v[1] * sc), pack_f16(v[2] * sc, v[3] * sc), pack_f16(v[4] * sc, v[5] * sc),
-                   pack_f16(v[6] * sc, v[7] * sc));
-  }
-  if (t == 0) a.image_info[image] = (mx > 0.f ? e + kInfoBias : 0) | (static_cast<int>(s_pages) << 8) | (odd ? kInfoOdd : 0);
 }
 
 // ---- attend -------------------------------------------------------------------------------------
@@ -1036,7 +1041,8 @@ void window_attach_images(WindowArgs* a, void* workspace, int64_t slots) {
 }
 
 cudaError_t launch_window_prefill_tc(const WindowArgs& a, const CUtensorMap& q_map, int sms, cudaStream_t stream) {
-  const dim3 grid(static_cast<unsigned>(a.image_slots), static_cast<unsigned>(a.num_kv_heads));
+  const int most = kMaxConvertCtas / a.num_kv_heads;
+  const dim3 grid(static_cast<unsigned>(max(1, min(a.image_slots, most))), static_cast<unsigned>(a.num_kv_heads));
   switch (a.kv_dtype) {
     case PBS_KV_BF16: convert_kernel<PBS_KV_BF16><<<grid, 512, 0, stream>>>(a); break;
     case PBS_KV_FP8_E4M3: convert_kernel<PBS_KV_FP8_E4M3><<<grid, 512, 0, stream>>>(a); break;

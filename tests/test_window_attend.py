@@ -443,6 +443,53 @@ def test_prefill_calls_on_two_streams_at_once(kv):
 
 
 @gpu
+@pytest.mark.parametrize("kv", FMT)
+@pytest.mark.parametrize("window,sinks", [(0, 0), (130, 20)])
+def test_prefill_in_parts(kv, window, sinks, monkeypatch):
+    """A workspace for one or some of the requests: the same bits as with all of it; for less: the other kernel."""
+    c = Case(kv, 2, 4, [(40, 300), (1, 1), (130, 130), (0, 77), (70, 500)], window, sinks, seed=31)
+    d, e = c.dev(), err()
+    n, mb = len(c.reqs), c.max_blocks
+    want = prefill(c, d, return_lse=True, err_word=e)
+    check(*want, c.want())
+    size = lambda reqs: pbs.window_prefill_workspace_bytes(c.total_q, reqs, c.hkv, mb, kv, window, sinks)
+    for reqs in range(1, n):
+        assert size(reqs) < size(n)
+        ws = torch.empty(size(reqs), dtype=torch.uint8, device="cuda")
+        got = prefill(c, d, return_lse=True, err_word=e, workspace=ws)
+        assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    small = torch.empty(size(1) - 256, dtype=torch.uint8, device="cuda")
+    check(*prefill(c, d, return_lse=True, err_word=e, workspace=small), c.want())
+    for cap in (size(2), size(1) - 256):
+        monkeypatch.setattr(pbs, "WINDOW_WORKSPACE_CAP", cap)
+        pbs._window_workspaces.clear()
+        got = prefill(c, d, return_lse=True, err_word=e)
+        check(*got, c.want())
+    pbs._window_workspaces.clear()
+    assert int(e) == 0
+
+
+@gpu
+def test_prefill_with_more_images_than_the_conversion_has_blocks():
+    """40 blocks x 512 kv heads. Both kernels are within 2^-8 |o| + mass (2^-10 + 2 logit) of the true value (see
+    check), mass <= max |V| and logit <= 2^-16 * 16 here: twice that between them."""
+    hkv, blocks = 512, 40
+    g = torch.Generator(device="cuda").manual_seed(5)
+    cache = torch.empty(blocks * 8, hkv * 16 * 256, dtype=torch.uint8, device="cuda")
+    for i in range(0, blocks * 8, 8):
+        cache[i:i + 8] = torch.randn(8, hkv * 16 * 256, device="cuda", generator=g).to(torch.float8_e4m3fn).view(torch.uint8)
+    q = torch.randn(5, hkv, 128, device="cuda", generator=g).to(torch.bfloat16)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    table = torch.randperm(blocks, device="cuda", generator=g).int()[None]
+    cu, lens = torch.tensor([0, 5], **i32), torch.tensor([blocks * 128 - 3], **i32)
+    got, want = (pbs.window_prefill_attention(q, cache, "fp8_e4m3", hkv, table, cu, lens, 128 ** -0.5, workspace=w).float()
+                 for w in ("auto", None))
+    pbs._window_workspaces.clear()
+    vmax = cache.view(torch.float8_e4m3fn).float().abs().max()
+    assert ((got - want).abs() <= 2 * (2.0 ** -8 * want.abs() + vmax * (2.0 ** -10 + 2.0 ** -11))).all()
+
+
+@gpu
 def test_empty_calls_leave_nothing_behind():
     c = Case("bf16", 2, 4, [(2, 40)], 16, 2)
     d = c.dev()
