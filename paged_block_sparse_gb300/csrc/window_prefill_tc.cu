@@ -31,8 +31,8 @@
 // thread and the softmax's code than it saved (703 -> 744 us); so did two threads per row (972 us: 96 to 104
 // registers a thread spill).
 //
-// Measured (events, L2 flushed): prompts of 2k-8k tokens, bf16, 64 / 8 heads, window 1024 + 64 sinks 714 us =
-// 1016 TFLOP/s on the keys that are seen, 52 % of the measured dense rate (38 us of it the images); 2 x 4096
+// Measured (events, L2 flushed): prompts of 2k-8k tokens, bf16, 64 / 8 heads, window 1024 + 64 sinks 706 us =
+// 1028 TFLOP/s on the keys that are seen, 53 % of the measured dense rate (38 us of it the images); 2 x 4096
 // tokens after 16k and 32k, NVFP4, 64 / 4 heads, window 4096 + 128 sinks 783 us = 1448 TFLOP/s, 75 %. A step (one
 // block, both tiles) takes 2.9k clk for 2048 clk of MMAs: each tile's chain is its softmax (1300), PV and S
 // (512 each) and 600 of barrier and MMA latency. A tile's end costs 5k clk.
@@ -439,9 +439,37 @@ __device__ __forceinline__ void add_odd_values(const uint8_t* page, int g, int r
   }
 }
 
+// add_odd_values for the keys that a row at position p sees, over its MMA tile's blocks.
+__device__ __noinline__ void add_odd_blocks(const WindowArgs& a, const Tile& t, int2 range, int p, uint16_t* own) {
+#pragma unroll 1
+  for (int i = 0; i < t.count; ++i) {
+    if (i >= t.head && (i < range.x || i > range.y)) continue;
+    const int b = tile_block(t, i);
+    const int info = __ldg(a.image_info + static_cast<int64_t>(t.slot0 + (b < t.req_head ? b : t.req_head + b - t.req_first)) *
+                                              a.num_kv_heads + t.g);
+    if (!(info & kInfoOdd)) continue;
+    const int64_t p0 = static_cast<int64_t>(__ldg(a.page_table + static_cast<int64_t>(t.req) * a.pt_row_stride + b)) *
+                       a.block_page_stride;
+#pragma unroll 1
+    for (int c = 0; c < 4; ++c) {
+      uint32_t w = row_bits(a, b * kSparseBlock + 32 * c, p, true, info >> (8 + 2 * c));
+#pragma unroll 1
+      for (; w != 0; w &= w - 1) {
+        const int key = 32 * c + __ffs(w) - 1;
+        const uint8_t* page = a.kv_cache + (p0 + key / kPageRows) * a.page_stride_bytes;
+        switch (a.kv_dtype) {
+          case PBS_KV_BF16: add_odd_values<PBS_KV_BF16>(page, t.g, key % kPageRows, a.v_scale, own); break;
+          case PBS_KV_FP8_E4M3: add_odd_values<PBS_KV_FP8_E4M3>(page, t.g, key % kPageRows, a.v_scale, own); break;
+          default: add_odd_values<PBS_KV_NVFP4>(page, t.g, key % kPageRows, a.v_scale, own);
+        }
+      }
+    }
+  }
+}
+
 template <int kG>
 __global__ void __launch_bounds__(kThreadsTc, 1)
-    prefill_kernel(const __grid_constant__ CUtensorMap q_map, const WindowArgs a) {
+    prefill_kernel(const __grid_constant__ CUtensorMap q_map, const __grid_constant__ WindowArgs a) {
   constexpr int T = kRows / kG;
   extern __shared__ __align__(1024) uint8_t smem[];
   if ((smem_u32(smem) & 1023u) != 0) {  // the swizzled operands need it
@@ -705,30 +733,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
       if (odd) {
         __syncwarp();
         uint16_t* own = a.out + (row0 + tok) * a.out_row_stride + static_cast<int64_t>(head0 + h) * a.out_head_stride;
-#pragma unroll 1
-        for (int i = 0; live && i < t.count; ++i) {
-          if (i >= t.head && (i < range.x || i > range.y)) continue;
-          const int b = tile_block(t, i);
-          const int info = __ldg(a.image_info + static_cast<int64_t>(t.slot0 + (b < t.req_head ? b : t.req_head + b - t.req_first)) *
-                                                    a.num_kv_heads + t.g);
-          if (!(info & kInfoOdd)) continue;
-          const int64_t p0 = static_cast<int64_t>(__ldg(a.page_table + static_cast<int64_t>(t.req) * a.pt_row_stride + b)) *
-                             a.block_page_stride;
-#pragma unroll 1
-          for (int c = 0; c < 4; ++c) {
-            uint32_t w = row_bits(a, b * kSparseBlock + 32 * c, p, true, info >> (8 + 2 * c));
-#pragma unroll 1
-            for (; w != 0; w &= w - 1) {
-              const int key = 32 * c + __ffs(w) - 1;
-              const uint8_t* page = a.kv_cache + (p0 + key / kPageRows) * a.page_stride_bytes;
-              switch (a.kv_dtype) {
-                case PBS_KV_BF16: add_odd_values<PBS_KV_BF16>(page, t.g, key % kPageRows, a.v_scale, own); break;
-                case PBS_KV_FP8_E4M3: add_odd_values<PBS_KV_FP8_E4M3>(page, t.g, key % kPageRows, a.v_scale, own); break;
-                default: add_odd_values<PBS_KV_NVFP4>(page, t.g, key % kPageRows, a.v_scale, own);
-              }
-            }
-          }
-        }
+        if (live) add_odd_blocks(a, t, range, p, own);
         __syncwarp();
         if (!next_tile(k + 1)) break;
       }
@@ -884,8 +889,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
     }
   } else if (warp == 1) {
     // ------------------------------------------------------------------ MMAs
-    // Step n of the CTA's block sequence, over its tiles: PV_A(n - 1) S_A(n) PV_B(n - 1) S_B(n). A tile's first S
-    // goes out between the last PVs of the tile before it.
+    // Step n of the CTA's block sequence, over its tiles: PV_A(n - 1) S_A(n) PV_B(n - 1) S_B(n).
     if (elect_one()) {
       constexpr uint32_t kIdescS = tc::idesc_f16(128, 128, true, false, false);
       constexpr uint32_t kIdescPV = tc::idesc_f16(128, 128, false, false, true);
@@ -950,37 +954,57 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
           if (!ok) break;
           qk(1);
         } else {
-          // both PVs first: S of the next tile may have to wait for its Q
-          ok = pv(0) && pv(1);
-          while (ok) {  // the next tile, skipping those without blocks
-            ++k;
-            ok = wait_on(&ctl->tile_full[k & 1], (k >> 1) & 1, ctl, a.err_word);
-            if (!ok) break;
-            const Tile* t = &ctl->tile[k & 1];
-            end = t->end != 0;
-            count = end ? 0 : t->count;
+          // S_A of the next tile goes before PV_B, unless its description is late or it has no blocks (the wait for the
+          // tile after it could depend on PV_B)
+          const auto enter = [&](const Tile* t) {
+            count = t->count;
             head = t->head;
-            if (!end) {
-              r[0] = seen_range<kG>(a, *t, 0);
-              r[1] = seen_range<kG>(a, *t, 1);
-            }
+            r[0] = seen_range<kG>(a, *t, 0);
+            r[1] = seen_range<kG>(a, *t, 1);
             mbar_arrive(&ctl->tile_empty[k & 1]);
-            if (end) break;
-            ok = wait_on(&ctl->q_full[0], k & 1, ctl, a.err_word);
-            if (!ok || count > 0) break;
-            ok = wait_on(&ctl->q_full[1], k & 1, ctl, a.err_word);
-            mbar_arrive(&ctl->q_empty[0]);
-            mbar_arrive(&ctl->q_empty[1]);
-          }
+          };
+          ok = pv(0);
           if (!ok) break;
-          if (!end) {
-            fresh[0] = fresh[1] = true;
+          const Tile* next = &ctl->tile[(k + 1) & 1];
+          if (mbar_try_wait(&ctl->tile_full[(k + 1) & 1], ((k + 1) >> 1) & 1) && !next->end && next->count > 0 &&
+              wait_on(&ctl->q_full[0], (k + 1) & 1, ctl, a.err_word)) {
+            ++k;
+            enter(next);
+            fresh[0] = true;
             ok = k_ready || wait_on(&ctl->full[st], ph, ctl, a.err_word);
             if (!ok) break;
             qk(0);
-            ok = wait_on(&ctl->q_full[1], k & 1, ctl, a.err_word);
+            ok = pv(1);
+            fresh[1] = true;
+            ok = ok && wait_on(&ctl->q_full[1], k & 1, ctl, a.err_word);
             if (!ok) break;
             qk(1);
+          } else {
+            ok = pv(1);
+            while (ok) {  // the next tile, skipping those without blocks
+              ++k;
+              ok = wait_on(&ctl->tile_full[k & 1], (k >> 1) & 1, ctl, a.err_word);
+              if (!ok) break;
+              const Tile* t = &ctl->tile[k & 1];
+              end = t->end != 0;
+              if (end) break;
+              enter(t);
+              ok = wait_on(&ctl->q_full[0], k & 1, ctl, a.err_word);
+              if (!ok || count > 0) break;
+              ok = wait_on(&ctl->q_full[1], k & 1, ctl, a.err_word);
+              mbar_arrive(&ctl->q_empty[0]);
+              mbar_arrive(&ctl->q_empty[1]);
+            }
+            if (!ok) break;
+            if (!end) {
+              fresh[0] = fresh[1] = true;
+              ok = k_ready || wait_on(&ctl->full[st], ph, ctl, a.err_word);
+              if (!ok) break;
+              qk(0);
+              ok = wait_on(&ctl->q_full[1], k & 1, ctl, a.err_word);
+              if (!ok) break;
+              qk(1);
+            }
           }
         }
         if (!ok) break;
