@@ -677,16 +677,20 @@ def _decode_workspace_need(device, *shape):
         return int(lib().pbs_window_decode_workspace_bytes(*shape))
 
 
-def _window_workspace(kind, need, device, stream):
+def _window_workspace(kind, need, device, stream, tickets=0):
     """The cached workspace of (kind, device, stream), grown on demand. Calls on one stream run in
     order, so they may share it; a call under graph capture gets memory of the graph's own, so that
-    graphs captured on one stream may be replayed side by side."""
+    graphs captured on one stream may be replayed side by side. tickets: bytes at its end that start
+    at zero (a graph clears them at each replay: its memory may have served others since)."""
     if stream is not None:
         with torch.cuda.stream(stream):
-            return _window_workspace(kind, need, device, None)
-    make = torch.zeros if kind == "decode" else torch.empty
+            return _window_workspace(kind, need, device, None, tickets)
     if torch.cuda.is_current_stream_capturing():
-        return make(need, dtype=torch.uint8, device=device)
+        ws = torch.empty(need, dtype=torch.uint8, device=device)
+        if tickets:
+            ws[-min(tickets, need):].zero_()
+        return ws
+    make = torch.zeros if tickets else torch.empty
     key = (kind, device.index, torch._C._cuda_getCurrentRawStream(device.index))
     ws = _window_workspaces.get(key)
     if ws is None or ws.numel() < need:
@@ -740,7 +744,8 @@ def window_decode_attention(q, kv_cache, kv_dtype: str, num_kv_heads: int, page_
         if workspace != "auto":
             raise ValueError('workspace must be "auto", None or a uint8 CUDA tensor')
         need = _decode_workspace_need(dev, batch, dql, hq, hkv)
-        workspace = _window_workspace("decode", need, dev, stream) if need else None
+        # (a ticket per group of rows and kv head)
+        workspace = _window_workspace("decode", need, dev, stream, 4 * batch * dql * hkv) if need else None
     wp, wb = (None, 0) if workspace is None else (_vec(workspace, "workspace", dev, torch.uint8), workspace.numel())
     _call(dev, L.pbs_window_decode_attention, "pbs_window_decode_attention",
           q.data_ptr(), q.stride(0), q.stride(1), kv_cache.data_ptr(), kv_cache.stride(0) * kv_cache.element_size(),
