@@ -31,9 +31,9 @@
 // thread and the softmax's code than it saved (703 -> 744 us); so did two threads per row (972 us: 96 to 104
 // registers a thread spill).
 //
-// Measured (events, L2 flushed): prompts of 2k-8k tokens, bf16, 64 / 8 heads, window 1024 + 64 sinks 706 us =
-// 1028 TFLOP/s on the keys that are seen, 53 % of the measured dense rate (38 us of it the images); 2 x 4096
-// tokens after 16k and 32k, NVFP4, 64 / 4 heads, window 4096 + 128 sinks 783 us = 1448 TFLOP/s, 75 %. A step (one
+// Measured (events, L2 flushed): prompts of 2k-8k tokens, bf16, 64 / 8 heads, window 1024 + 64 sinks 701 us =
+// 1035 TFLOP/s on the keys that are seen, 53 % of the measured dense rate (38 us of it the images); 2 x 4096
+// tokens after 16k and 32k, NVFP4, 64 / 4 heads, window 4096 + 128 sinks 779 us = 1456 TFLOP/s, 75 %. A step (one
 // block, both tiles) takes 2.9k clk for 2048 clk of MMAs: each tile's chain is its softmax (1300), PV and S
 // (512 each) and 600 of barrier and MMA latency. A tile's end costs 5k clk.
 #include "mbar_wait.cuh"
@@ -661,12 +661,12 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
           }
           tc::st16(ts + 16 * c, pk);
         }
-        l += (sum0.x + sum0.y + sum1.x + sum1.y) * exp2i(-de);
         started = true;
         tc::wait_st();
         tc::fence_before_sync();
         __syncwarp();
         if (lane == 0) mbar_arrive(&ctl->p_full[x]);
+        l += (sum0.x + sum0.y + sum1.x + sum1.y) * exp2i(-de);
         ++ns;
       }
       if (!ok) break;
