@@ -471,6 +471,7 @@ PBS_API size_t pbs_window_decode_workspace_bytes(int32_t batch, int32_t decode_q
  *                scales) the call runs on the tcgen05 kernel, otherwise on the decode kernel (mma.sync). With
  *                less it takes the requests in parts, as many at a time as it holds (the size that the query
  *                gives for them); less than one request's is not used. Calls that share one workspace must not run concurrently.
+ * The tcgen05 kernel holds a key's softmax weight in fp16: one below 2^-24 of the row's largest counts as 0.
  */
 PBS_API int pbs_window_prefill_attention(
     const void* q, int64_t q_row_stride, int64_t q_head_stride,

@@ -23,7 +23,7 @@
 //    P is rounded to fp16 (2^-11; bf16's 2^-8 would double the error of a bf16 output), sums stay in fp32.
 //    Online softmax in base 2: the reference moves, and O is rescaled, only when the row maximum passes
 //    it by 2^8. Each row keeps the exponent E of its O (O holds sum(P V) * 2^-E); a block of exponent e
-//    enters as P * 2^(e - E), and E moves when e - E leaves [-8, 7].
+//    enters as P * 2^(e - E), and E moves when e - E leaves [-8, 7] (down only as far as O's fp32 has room).
 //    A row without a key of its own in some block keeps m = -inf there; infinities and NaN in V are cleared in
 //    the images (0 * NaN would reach rows that do not see them) and added to the rows that do, after the output.
 // Blocks are masked per row only where a row's border crosses them; a block that no row of A (or B) sees is
@@ -53,6 +53,7 @@ constexpr int kRing = 4;
 constexpr int kOutStage = 8 * 4096;   // 32 rows x 64 dims of bf16 per softmax warp
 constexpr float kLazyLog2 = 8.0f;
 constexpr int kExpUp = 7, kExpDown = -8;
+constexpr int kNoExp = -1000;  // E before the row's first block (far from any)
 constexpr unsigned long long kWaitNs = 100000000ull;
 // block info word: V exponent + 128 in the low byte (0: no finite V but zeros), valid pages in the next,
 // then whether some V is infinite or NaN
@@ -535,7 +536,8 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
       // positions of the warp's rows (those without a token count: they are not written)
       const int pw0 = pa + quad * 32 / kG, pw1 = pa + (quad * 32 + 31) / kG;
       float m = -INFINITY, l = 0.f;
-      int E = 0;
+      int E = kNoExp;
+      int top = 0;  // at E's last move: the largest V (its e) that O held, by weight
       bool started = false;  // the tile has had a block: O holds something
       int odd = 0;           // kInfoOdd: one of them has infinities or NaN in V
       const int2 range = seen_range<kG>(a, t, x);
@@ -618,19 +620,26 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
           m = mxs;
         }
         const int e = info & 0xff;
-        int de = 0;
-        if (any && e != 0) {
-          de = e - kInfoBias - E;
-          if (!started || (de > kExpUp || (de < kExpDown && de >= -100))) {
-            if (started) f *= exp2i(-de);
-            E += de;
-            de = 0;
+        const bool some = any && e != 0;
+        int de = some ? e - kInfoBias - E : 0;
+        const bool moves = static_cast<uint32_t>(de - kExpDown) > static_cast<uint32_t>(kExpUp - kExpDown);  // not in [-8, 7]
+        if (__any_sync(0xffffffffu, f != 1.f || moves)) {
+          if (some) {
+            const int lost = f > 0.f ? static_cast<int>(-log2f(f)) : 512;
+            const int held = max(top, E + kInfoBias) - lost;  // largest V that O holds, by weight (within 2^7)
+            if (E == kNoExp || f == 0.f) {  // nothing of the row
+              E += de;
+              de = 0;
+              top = e;
+            } else if (de > kExpUp || (de < kExpDown && de >= -120 && e >= held - 40)) {
+              f *= exp2i(-de);  // (no lower than 40 below what O holds: it cannot overflow)
+              E += de;
+              de = 0;
+              top = max(held, e);
+            }
           }
-          de = max(de, -60);  // V that far below O adds nothing; the row sum still counts its keys
-        }
-        if (__any_sync(0xffffffffu, f != 1.f)) {
           // (S(i) complete: so is the tile's PV(i - 1), issued before it)
-          if (started) {
+          if (started && __any_sync(0xffffffffu, f != 1.f)) {
 #pragma unroll 1
             for (int c = 0; c < 128; c += 16) {  // few registers: the scores stay in theirs
               uint32_t o[16];
@@ -642,6 +651,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
             }
           }
         }
+        de = max(de, -60);  // V that far below O adds nothing; the row sum still counts its keys
         // P * 2^de, and the row sum
         const float mu = (m == -INFINITY ? 0.f : m) - static_cast<float>(de);
         float2 sum0 = make_float2(0.f, 0.f), sum1 = make_float2(0.f, 0.f);
@@ -682,6 +692,7 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
       tc::fence_after_sync();
       // O * 2^E * v_scale / l. The factor stays in fp32's range for |E| <= 60; beyond, 2^E goes in two steps.
       const float inv = l != 0.f ? a.v_scale / l : 0.f;
+      if (E == kNoExp) E = 0;
       const int e1 = max(-60, min(60, E));
       const float f1 = inv * exp2i(e1), f2 = exp2i(E - e1);
       const bool far = __any_sync(0xffffffffu, E != e1);

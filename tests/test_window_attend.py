@@ -397,6 +397,25 @@ def test_prefill_values_of_any_size(kv):
 
 
 @gpu
+def test_prefill_values_that_shrink_along_a_long_context():
+    """80 blocks of V around 2^50, then smaller and smaller ones, all of one weight (q = 0): sums near 2^63, to
+    which the last blocks add nothing."""
+    c = Case("bf16", 1, 8, [(3, 10900)], 0, 0, seed=17)
+    c.q.zero_()
+    shift = {80: 2, 81: -20, 82: -38, 83: -45, 84: -80, 85: -90}
+    for b in range(c.max_blocks):
+        for page in range(int(c.table[0, b]) * 8, int(c.table[0, b]) * 8 + 8):
+            if page in c.pages:
+                rows = c.pages[page].reshape(16, 512)[:, 256:]
+                v = torch.from_numpy(rows.copy()).view(torch.bfloat16)
+                v = torch.where(v.isnan(), v, (v.float() * 2.0 ** shift.get(b, 50)).to(torch.bfloat16))
+                rows[:] = v.view(torch.uint8).numpy()
+    d = c.dev()
+    out, lse = prefill(c, d, return_lse=True)
+    check(out, lse, c.want())
+
+
+@gpu
 def test_prefill_captured():
     c = Case("nvfp4", 1, 8, [(60, 500), (1, 9)], 200, 4, seed=11)
     d = c.dev()
