@@ -24,16 +24,15 @@
 //    Online softmax in base 2: the reference moves, and O is rescaled, only when the row maximum passes
 //    it by 2^8. Each row keeps the exponent E of its O (O holds sum(P V) * 2^-E); a block of exponent e
 //    enters as P * 2^(e - E), and E moves when e - E leaves [-8, 7] (down only as far as O's fp32 has room).
-//    A row without a key of its own in some block keeps m = -inf there; infinities and NaN in V are cleared in
-//    the images (0 * NaN would reach rows that do not see them) and added to the rows that do, after the output.
+//    Infinities and NaN in V are cleared in the images (0 * NaN would reach rows that do not see them) and added to the rows that do, after the output.
 // Blocks are masked per row only where a row's border crosses them; a block that no row of A (or B) sees is
 // skipped for it. Multiplying just the 32-key parts of a crossed block that some row sees cost more in the MMA
 // thread and the softmax's code than it saved (703 -> 744 us); so did two threads per row (972 us: 96 to 104
 // registers a thread spill).
 //
-// Measured (events, L2 flushed): prompts of 2k-8k tokens, bf16, 64 / 8 heads, window 1024 + 64 sinks 701 us =
-// 1035 TFLOP/s on the keys that are seen, 53 % of the measured dense rate (38 us of it the images); 2 x 4096
-// tokens after 16k and 32k, NVFP4, 64 / 4 heads, window 4096 + 128 sinks 779 us = 1456 TFLOP/s, 75 %. A step (one
+// Measured (events, L2 flushed): prompts of 2k-8k tokens, bf16, 64 / 8 heads, window 1024 + 64 sinks 703 us =
+// 1032 TFLOP/s on the keys that are seen, 53 % of the measured dense rate (38 us of it the images); 2 x 4096
+// tokens after 16k and 32k, NVFP4, 64 / 4 heads, window 4096 + 128 sinks 775 us = 1463 TFLOP/s, 75 %. A step (one
 // block, both tiles) takes 2.9k clk for 2048 clk of MMAs: each tile's chain is its softmax (1300), PV and S
 // (512 each) and 600 of barrier and MMA latency. A tile's end costs 5k clk.
 #include "mbar_wait.cuh"
