@@ -24,7 +24,8 @@
 //    Online softmax in base 2: the reference moves, and O is rescaled, only when the row maximum passes
 //    it by 2^8. Each row keeps the exponent E of its O (O holds sum(P V) * 2^-E); a block of exponent e
 //    enters as P * 2^(e - E), and E moves when e - E leaves [-8, 7] (down only as far as O's fp32 has room).
-//    Infinities and NaN in V are cleared in the images (0 * NaN would reach rows that do not see them) and added to the rows that do, after the output.
+//    Infinities and NaN in V are cleared in the images (0 * NaN would reach rows that do not see them) and
+//    added, after the output, to the rows that do.
 // Blocks are masked per row only where a row's border crosses them; a block that no row of A (or B) sees is
 // skipped for it. Multiplying just the 32-key parts of a crossed block that some row sees cost more in the MMA
 // thread and the softmax's code than it saved (703 -> 744 us); so did two threads per row (972 us: 96 to 104
