@@ -490,7 +490,8 @@ __global__ void __launch_bounds__(Cfg<FMT, NT>::kThreads, Cfg<FMT, NT>::kCtas)
           for (int t = 0; t < NT; ++t)
 #pragma unroll
             for (int w = 0; w < 2; ++w) {
-              const uint32_t b = ((real >> i) & 1u) && row_of[t][w] < it.rows ? seen_bits(a, n0, it.p0 + row_of[t][w], it.p0 + row_of[t][w]) : 0u;
+              const int p = it.p0 + row_of[t][w];
+              const uint32_t b = ((real >> i) & 1u) && row_of[t][w] < it.rows ? seen_bits(a, n0, p, p) : 0u;
               if (!((b >> hh) & 1u)) sc[i][t][w] = -INFINITY;
               if (!((b >> (hh + 8)) & 1u)) sc[i][t][w + 2] = -INFINITY;
             }

@@ -720,7 +720,8 @@ __global__ void __launch_bounds__(kThreadsTc, 1)
           uint32_t w[4];
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const float2 y = mul2(make_float2(__uint_as_float(o[8 * q + 2 * j]), __uint_as_float(o[8 * q + 2 * j + 1])), make_float2(f1, f1));
+            const int d = 8 * q + 2 * j;
+            const float2 y = mul2(make_float2(__uint_as_float(o[d]), __uint_as_float(o[d + 1])), make_float2(f1, f1));
             w[j] = pack_bf16(y.x, y.y);
           }
           *reinterpret_cast<uint4*>(stage + lane * 128 + ((q ^ (lane & 7)) << 4)) = make_uint4(w[0], w[1], w[2], w[3]);
